@@ -30,11 +30,15 @@ LAYOUT_CONTIGUOUS, LAYOUT_MASKED = 0, 1
 EPI_BF16, EPI_SWIGLU_FP8 = 0, 1
 CONTIG_AUTO, CONTIG_SINGLE, CONTIG_PAIR = 0, 1, 2
 WEIGHTS_FP8, WEIGHTS_W4 = 0, 1
+TYPE_BF16, TYPE_FP32 = 0, 1
 EXPORTS = ("moe_rows_capacity", "moe_workspace_size", "moe_route", "moe_permute", "moe_grouped_gemm_fp8",
            "moe_combine", "moe_forward", "moe_forward_train", "moe_get_device_status", "moe_selftest_wait_timeout", "moe_status_string",
            "moe_permute_noalloc", "moe_balance_bias", "moe_grouped_gemm_w4", "moe_set_contig_kernel",
            "moe_ep_plan", "moe_ep_plan_chunked", "moe_ep_workspace_size", "moe_ep_count", "moe_ep_dispatch",
-           "moe_ep_receive", "moe_ep_receive_chunk", "moe_ep_return", "moe_backward_workspace_size", "moe_backward")
+           "moe_ep_receive", "moe_ep_receive_chunk", "moe_ep_return", "moe_backward_workspace_size", "moe_backward",
+           "moe_train_logits_offset", "moe_balance_workspace_size", "moe_balance_loss", "moe_balance_loss_backward",
+           "moe_router_backward_workspace_size", "moe_router_backward", "moe_orthogonalise_workspace_size",
+           "moe_orthogonalise")
 
 
 class MoeError(RuntimeError):
@@ -68,9 +72,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB)
         P, I, SZ, CP = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.POINTER(Config)
         L.moe_rows_capacity.argtypes = [CP]
-        L.moe_rows_capacity.restype = SZ
         L.moe_workspace_size.argtypes = [CP, I]
-        L.moe_workspace_size.restype = SZ
         L.moe_route.argtypes = [CP, P, P, P, P, P, P, P, SZ, P]
         L.moe_permute.argtypes = [CP, P, P, P, P, P, P, P, P, P, P, SZ, P]
         L.moe_permute_noalloc.argtypes = [CP, P, P, P, P, P, P, P, P, P, P]
@@ -86,20 +88,31 @@ def lib() -> ctypes.CDLL:
         L.moe_ep_plan.argtypes = [I, I, I, ctypes.c_int64, I, I, I, P, P]
         L.moe_ep_plan_chunked.argtypes = [I, I, I, ctypes.c_int64, I, I, I, P, I, P]
         L.moe_ep_workspace_size.argtypes = [CP]
-        L.moe_ep_workspace_size.restype = SZ
         L.moe_ep_count.argtypes = [CP, P, P, P, SZ, P]
         L.moe_ep_dispatch.argtypes = [CP, P, P, P, P, P, P, SZ, P]
         L.moe_ep_receive.argtypes = [I, P, I, P, P, P, I, P, P, P]
         L.moe_ep_receive_chunk.argtypes = [I, P, I, P, P, P, I, P, P, P]
         L.moe_ep_return.argtypes = [I, I, P, P, P, P]
         L.moe_backward_workspace_size.argtypes = [CP]
-        L.moe_backward_workspace_size.restype = SZ
         L.moe_backward.argtypes = [CP] + [P] * 12 + [I] + [P] * 7 + [SZ, P]
+        F = ctypes.c_float
+        L.moe_train_logits_offset.argtypes = [CP]
+        L.moe_balance_workspace_size.argtypes = [I, I, I]
+        L.moe_balance_loss.argtypes = [I, I, I, P, P, P, P, I, F, F, P, P, P, P, P, P, SZ, P]
+        L.moe_balance_loss_backward.argtypes = [I, I, I, P, P, P, P, P, P, I, F, F, P, P, P]
+        L.moe_router_backward_workspace_size.argtypes = [I, I, I]
+        L.moe_router_backward.argtypes = [I, I, I] + [P] * 10 + [SZ, P]
+        L.moe_orthogonalise_workspace_size.argtypes = [I, I, I, I]
+        L.moe_orthogonalise.argtypes = [I, I, I, I, P, I, I, F, F, F, F, F, P, P, SZ, P]
+        sizes = ("moe_rows_capacity", "moe_workspace_size", "moe_ep_workspace_size", "moe_backward_workspace_size",
+                 "moe_train_logits_offset", "moe_balance_workspace_size", "moe_router_backward_workspace_size",
+                 "moe_orthogonalise_workspace_size")
+        for f in sizes:
+            getattr(L, f).restype = SZ
         L.moe_status_string.argtypes = [I]
         L.moe_status_string.restype = ctypes.c_char_p
         for f in EXPORTS:
-            if f not in ("moe_rows_capacity", "moe_workspace_size", "moe_status_string", "moe_ep_workspace_size",
-                         "moe_backward_workspace_size"):
+            if f != "moe_status_string" and f not in sizes:
                 getattr(L, f).restype = I
         _lib = L
     return _lib
@@ -257,3 +270,56 @@ def moe_backward(cfg, x, Wg, W13, S13, W13T, S13T, W2T, S2T, topk_idx, topk_w, s
                               _p(S2T), _p(topk_idx), _p(topk_w), _p(slot_row), _p(fwd_ws), int(bool(fwd_train)),
                               _p(dy), _p(dx), _p(dWg), _p(db), _p(dW13), _p(dW2), _p(ws), _nbytes(ws),
                               _stream(stream)), "moe_backward")
+
+
+# ---------------------------------------------------------------- balance loss, the router's gradient, updates
+def moe_train_logits(cfg: Config, ws: torch.Tensor) -> torch.Tensor:
+    """The router's logits [T, E] fp32 that moe_forward_train left in its workspace (a view of it)."""
+    off = int(lib().moe_train_logits_offset(ctypes.byref(cfg)))
+    if off == 0:
+        raise ValueError("moe_train_logits: not a configuration of moe_forward_train")
+    return ws[off:off + 4 * cfg.T * cfg.E].view(torch.float32).view(cfg.T, cfg.E)
+
+
+def moe_balance_workspace_size(T: int, E: int, S: int = 1) -> int:
+    return int(lib().moe_balance_workspace_size(T, E, S))
+
+
+def moe_balance_loss(T, E, k, logits, topk_idx, token_mask, seq_offsets, S, alpha, beta, loss, counts, mean_prob, lse,
+                     seq_valid, ws, stream=None):
+    """Balance loss and z-loss of the router's logits; token_mask, seq_offsets nullable."""
+    _check(lib().moe_balance_loss(T, E, k, _p(logits), _p(topk_idx), _p(token_mask), _p(seq_offsets), S, float(alpha),
+                                  float(beta), _p(loss), _p(counts), _p(mean_prob), _p(lse), _p(seq_valid), _p(ws),
+                                  _nbytes(ws), _stream(stream)), "moe_balance_loss")
+
+
+def moe_balance_loss_backward(T, E, k, logits, lse, counts, seq_valid, token_mask, seq_offsets, S, alpha, beta, dloss,
+                              dlogits, stream=None):
+    """dlogits [T, E] of moe_balance_loss; dloss [2] nullable (ones)."""
+    _check(lib().moe_balance_loss_backward(T, E, k, _p(logits), _p(lse), _p(counts), _p(seq_valid), _p(token_mask),
+                                           _p(seq_offsets), S, float(alpha), float(beta), _p(dloss), _p(dlogits),
+                                           _stream(stream)), "moe_balance_loss_backward")
+
+
+def moe_router_backward_workspace_size(T: int, H: int, E: int) -> int:
+    return int(lib().moe_router_backward_workspace_size(T, H, E))
+
+
+def moe_router_backward(T, H, E, x, Wg, dlogits, dx0, dWg0, db0, dx, dWg, db, ws, stream=None):
+    """dx = dx0 + dlogits Wg, dWg = dWg0 + dlogits^T x, db = db0 + sum of dlogits; the bases nullable."""
+    _check(lib().moe_router_backward(T, H, E, _p(x), _p(Wg), _p(dlogits), _p(dx0), _p(dWg0), _p(db0), _p(dx), _p(dWg),
+                                     _p(db), _p(ws), _nbytes(ws), _stream(stream)), "moe_router_backward")
+
+
+def moe_orthogonalise_workspace_size(batch: int, M: int, N: int, interleaved: bool = False) -> int:
+    return int(lib().moe_orthogonalise_workspace_size(batch, M, N, int(bool(interleaved))))
+
+
+def moe_orthogonalise(batch, M, N, interleaved, G, steps, a, b, c, eps, scale, O, ws, stream=None):
+    """O = scale * the quintic Newton-Schulz iterate of each matrix of G (bf16 or fp32) after `steps` steps."""
+    if G.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("moe_orthogonalise takes bf16 or fp32 matrices")
+    _check(lib().moe_orthogonalise(batch, M, N, int(bool(interleaved)), _p(G),
+                                   TYPE_FP32 if G.dtype == torch.float32 else TYPE_BF16, steps, float(a), float(b),
+                                   float(c), float(eps), float(scale), _p(O), _p(ws), _nbytes(ws), _stream(stream)),
+           "moe_orthogonalise")

@@ -148,6 +148,7 @@ struct FwdWs {
     int32_t* row_src;
     void* step;   // route / permute scratch
     uint16_t* ab; // training workspace only: the up GEMM's gate and up values, bf16 [rows, 2I]
+    float* logits; // the router's logits: kept in training, else in `step`, which the permutation reuses
     size_t total;
 };
 
@@ -171,8 +172,15 @@ FwdWs carve(const moe_config_t* c, void* base, bool train = false) {
     w.row_src = reinterpret_cast<int32_t*>(take(sizeof(int32_t) * rows));
     w.step = take(std::max(route_scratch(c), align_up(moe::permute_scratch_bytes(c->T, c->E))));
     w.ab = train ? reinterpret_cast<uint16_t*>(take(sizeof(uint16_t) * rows * 2 * c->I)) : nullptr;
+    w.logits = train ? reinterpret_cast<float*>(take(sizeof(float) * static_cast<size_t>(c->T) * c->E))
+                     : static_cast<float*>(w.step);
     w.total = off;
     return w;
+}
+
+// What the training forward takes (and with it the backward): contiguous layout, E4M3 weights, softmax routing.
+inline bool trainable(const moe_config_t* c) {
+    return c->layout == MOE_LAYOUT_CONTIGUOUS && c->weights == MOE_WEIGHTS_FP8 && c->routing == MOE_ROUTE_SOFTMAX_TOPK;
 }
 
 inline moe_status_t cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
@@ -258,12 +266,15 @@ size_t moe_rows_capacity(const moe_config_t* cfg) {
 
 size_t moe_workspace_size(const moe_config_t* cfg, int for_forward) {
     if (check_cfg(cfg) != MOE_OK || for_forward < 0 || for_forward > 2) return 0;
-    // the training forward takes what the backward takes: contiguous layout, E4M3 weights, softmax routing
-    if (for_forward == 2 && (cfg->layout != MOE_LAYOUT_CONTIGUOUS || cfg->weights != MOE_WEIGHTS_FP8 ||
-                             cfg->routing != MOE_ROUTE_SOFTMAX_TOPK))
-        return 0;
+    if (for_forward == 2 && !trainable(cfg)) return 0;
     if (for_forward) return carve(cfg, nullptr, for_forward == 2).total;
     return std::max(route_scratch(cfg), align_up(permute_scratch_bytes(cfg->T, cfg->E)));
+}
+
+size_t moe_train_logits_offset(const moe_config_t* cfg) {
+    if (check_cfg(cfg) != MOE_OK || !trainable(cfg)) return 0;
+    uint8_t* const base = reinterpret_cast<uint8_t*>(kAlign);   // never read: only the distance counts
+    return reinterpret_cast<uint8_t*>(carve(cfg, base, true).logits) - base;
 }
 
 moe_status_t moe_route(const moe_config_t* cfg, const void* x, const float* Wg, const float* bias,
@@ -373,9 +384,7 @@ static moe_status_t forward_impl(const moe_config_t* cfg, const void* x, const f
                                  int32_t* slot_row, void* ws, size_t ws_bytes, void* stream, bool train) {
     moe_status_t st = check_cfg(cfg);
     if (st != MOE_OK) return st;
-    if (train && (cfg->layout != MOE_LAYOUT_CONTIGUOUS || cfg->weights != MOE_WEIGHTS_FP8 ||
-                  cfg->routing != MOE_ROUTE_SOFTMAX_TOPK))
-        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (train && !trainable(cfg)) return MOE_ERR_UNSUPPORTED_SHAPE;
     DeviceInfo* dev;
     if ((st = device_info(&dev)) != MOE_OK) return st;
     if (!ptr_ok(x) || !ptr_ok(W13) || !ptr_ok(S13) || !ptr_ok(W2) || !ptr_ok(S2) || !ptr_ok(y) || !ptr_ok(topk_idx) ||
@@ -397,8 +406,8 @@ static moe_status_t forward_impl(const moe_config_t* cfg, const void* x, const f
     if (cfg->routing == MOE_ROUTE_HASH)
         e = launch_router_hash(token_ids, cfg->T, cfg->E, topk_idx, topk_w, s);
     else
-        e = launch_router_softmax(static_cast<const uint16_t*>(x), Wg, bias, static_cast<float*>(w.step), cfg->T,
-                                  cfg->H, cfg->E, cfg->k, topk_idx, topk_w, dev->status, kWaitNs, dev->num_sms, s);
+        e = launch_router_softmax(static_cast<const uint16_t*>(x), Wg, bias, w.logits, cfg->T, cfg->H,
+                                  cfg->E, cfg->k, topk_idx, topk_w, dev->status, kWaitNs, dev->num_sms, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     e = launch_permute(static_cast<const uint16_t*>(x), topk_idx, cfg->T, cfg->H, cfg->k, cfg->E, capacity_of(cfg),
                        masked ? cfg->masked_max_m : 0, rows, w.Aq, w.As, counts, w.kept, w.offsets, w.row_src,
@@ -441,9 +450,7 @@ moe_status_t moe_forward_train(const moe_config_t* cfg, const void* x, const flo
 // What moe_backward takes beyond a valid configuration: contiguous layout, E4M3 weights, softmax routing, and
 // K of the weight-gradient GEMMs (an expert's rows; 2I for g W13) within the 128 K blocks they stage.
 static moe_status_t check_backward_shape(const moe_config_t* cfg) {
-    if (cfg->layout != MOE_LAYOUT_CONTIGUOUS || cfg->weights != MOE_WEIGHTS_FP8 ||
-        cfg->routing != MOE_ROUTE_SOFTMAX_TOPK)
-        return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (!trainable(cfg)) return MOE_ERR_UNSUPPORTED_SHAPE;
     const int64_t most = cfg->cap_num ? std::min<int64_t>(cfg->T, capacity_of(cfg)) : cfg->T;
     if (most > 16384 || 2 * cfg->I > 16384) return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;

@@ -1,0 +1,492 @@
+// The router's balance loss and z-loss with their gradient with respect to the logits.
+//
+// p_t = softmax(l_t) over the E experts. For each sequence s (a run of tokens; a token mask leaves padding
+// out), n_s = its valid tokens, counts[s, e] = its slots routed to e, P[s, e] = mean of p_t[e]:
+//   loss0 = alpha / S' * sum_s sum_e f[s, e] P[s, e],  f = E counts / (k n_s),  S' = sequences with n_s > 0
+//   loss1 = beta / N * sum_t lse_t^2,                  lse_t = log sum_e exp(l_t[e]),  N = sum_s n_s
+// (the auxiliary loss over expert load fractions of the DeepSeek-V4 lecture page, 2.3, and the DeepSeek MoE
+// page, ch. 1, in its product form: counts are constants, the gradient flows through P). With upstream
+// gradients g0, g1 and c[s, e] = g0 alpha f / (S' n_s):
+//   dl_t[e] = p_t[e] (c[s, e] - sum_j p_t[j] c[s, j]) + 2 g1 beta / N lse_t p_t[e].
+//
+// Both passes read each logit once, and that read bounds them when T E is large; at a step's usual size the
+// 8 MB of logits sit in L2 and launches are the time, so the forward is two launches (the second resident
+// before the first ends) and the backward one. A group of 8 or 32 lanes takes a token: the row stays in
+// registers between its maximum, its sum and its use. The forward cuts the tokens into at most 296 chunks
+// (two blocks an SM); chunk c of sequence s leaves one row of partial sums at index c + s, which is unique
+// because the cuts between chunks and sequences, taken in order, each move c or s up by one. No float is
+// added atomically, so results repeat bit for bit.
+#include <math.h>
+
+#include <algorithm>
+
+#include "../../include/moe_fp8.h"
+#include "common.cuh"
+
+namespace moe {
+
+moe_status_t current_device(int* num_sms, int** status);
+
+namespace {
+
+constexpr int kBlThreads = 256;
+constexpr int kBlWarps = kBlThreads / 32;
+constexpr int kMaxChunks = 296;          // two 256-thread blocks on each of 148 SMs
+constexpr int kBwdTokens = 32;           // tokens a backward block takes at least
+
+// Tokens of a forward chunk: a multiple of 8, at most kMaxChunks chunks.
+int chunk_tokens(int T) { return std::max(8, ((T + kMaxChunks - 1) / kMaxChunks + 7) / 8 * 8); }
+int chunks_of(int T) { return (T + chunk_tokens(T) - 1) / chunk_tokens(T); }
+
+constexpr int kRedCols = 32, kRedRows = 16;   // the reducing blocks: columns x partial rows in flight
+
+// The forward's scratch: one row per (chunk, sequence) cut, and each reducing block's share of the loss.
+struct BalWs {
+    float* psum;        // [cuts, E] sums of p
+    int32_t* hist;      // [cuts, E] slots
+    float* zsum;        // [cuts] sums of lse^2
+    int32_t* nval;      // [cuts] valid tokens
+    double* part;       // [S, column blocks] sum_e counts * psum over the block's columns
+    double* zpart;      // [S]
+    unsigned* ticket;   // blocks of the reduction that are done
+    size_t total;
+};
+
+BalWs carve_balance(int T, int E, int S, void* base) {
+    BalWs w;
+    const size_t cuts = static_cast<size_t>(chunks_of(T)) + S, nx = (E + kRedCols - 1) / kRedCols;
+    uint8_t* p = static_cast<uint8_t*>(base);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t* q = p ? p + off : nullptr;
+        off += (bytes + 255) / 256 * 256;
+        return q;
+    };
+    w.psum = reinterpret_cast<float*>(take(4 * cuts * E));
+    w.hist = reinterpret_cast<int32_t*>(take(4 * cuts * E));
+    w.zsum = reinterpret_cast<float*>(take(4 * cuts));
+    w.nval = reinterpret_cast<int32_t*>(take(4 * cuts));
+    w.part = reinterpret_cast<double*>(take(8 * static_cast<size_t>(S) * nx));
+    w.zpart = reinterpret_cast<double*>(take(8 * static_cast<size_t>(S)));
+    w.ticket = reinterpret_cast<unsigned*>(take(4));
+    w.total = off;
+    return w;
+}
+
+// First token of sequence s (offsets[S]: one past the last), forced into [0, T]; no offsets: one sequence of all.
+__device__ __forceinline__ int seq_start(const int32_t* offsets, int s, int T) {
+    return offsets ? min(max(offsets[s], 0), T) : (s ? T : 0);
+}
+
+// The first sequence that ends behind token t (S if none does).
+__device__ __forceinline__ int seq_behind(const int32_t* offsets, int S, int T, int t) {
+    int lo = 0, hi = S;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (seq_start(offsets, mid + 1, T) > t) hi = mid; else lo = mid + 1;
+    }
+    return lo;
+}
+
+// Experts of a lane: value i of lane j of a G-lane group is expert 4 (j + G (i / 4)) + i % 4 where rows can
+// be read 16 bytes at a time (E a multiple of 4), else j + G i.
+template <int G, bool VEC>
+__device__ __forceinline__ int expert_of(int i, int j) {
+    return VEC ? 4 * (j + G * (i >> 2)) + (i & 3) : j + G * i;
+}
+
+template <int G, int V, bool VEC>
+__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int j, float fill, float (&v)[V]) {
+    if constexpr (VEC) {
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) {
+            const int e = 4 * (j + G * q);
+            float4 f = make_float4(fill, fill, fill, fill);
+            if (e < E) f = __ldg(reinterpret_cast<const float4*>(row + e));
+            v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = j + G * i < E ? __ldg(row + j + G * i) : fill;
+    }
+}
+
+// Sum and maximum over a G-lane group (every lane gets the result).
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ void dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_producer() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ---------------------------------------------------------------- forward, pass 1: partial sums of every cut
+// U tokens of each group are in flight together.
+template <int G, int V, bool VEC, int U>
+__global__ void __launch_bounds__(kBlThreads)
+balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
+                       const uint8_t* __restrict__ mask, const int32_t* __restrict__ offsets, int T, int E, int k,
+                       int S, int C, BalWs w, float* __restrict__ lse) {
+    constexpr int kGroups = 32 / G, kRows = kBlWarps * kGroups;     // tokens the block takes at a time
+    extern __shared__ float sm_red[];                               // [kRows][E]
+    __shared__ int sm_hist[kMaxE];
+    __shared__ float sm_z[kRows];
+    __shared__ int sm_n[kRows];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % G;
+    const int row = warp * kGroups + lane / G;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0;
+    dependents_may_launch();
+    const int c0 = blockIdx.x * C, c1 = min(c0 + C, T);
+    for (int s = seq_behind(offsets, S, T, c0); s < S; ++s) {
+        const int a = max(seq_start(offsets, s, T), c0), b = min(seq_start(offsets, s + 1, T), c1);
+        if (a >= c1) break;                          // this sequence, and with it every later one, starts behind
+        if (a >= b) continue;
+        for (int e = threadIdx.x; e < E; e += kBlThreads) sm_hist[e] = 0;
+        __syncthreads();
+        for (int i = threadIdx.x; i < (b - a) * k; i += kBlThreads) {
+            const int t = a + i / k;
+            const int e = idx[static_cast<int64_t>(a) * k + i];
+            if ((!mask || mask[t]) && e >= 0 && e < E) atomicAdd(&sm_hist[e], 1);
+        }
+        float acc[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+        float z = 0.0f;
+        int n = 0;
+        for (int t0 = a; t0 < b; t0 += kRows * U) {
+            float v[U][V];
+            bool on[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = t0 + u * kRows + row;
+                on[u] = t < b && (!mask || mask[t]);
+                load_row<G, V, VEC>(logits + static_cast<int64_t>(on[u] ? t : a) * E, E, j, -INFINITY, v[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float m = v[u][0];
+#pragma unroll
+                for (int i = 1; i < V; ++i) m = fmaxf(m, v[u][i]);   // a NaN comes back through the sum
+                m = group_max<G>(m);
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    // a lane's places behind the last expert hold -inf and give exp = 0, unless m is -inf too
+                    v[u][i] = expert_of<G, VEC>(i, j) < E ? expf(v[u][i] - m) : 0.0f;
+                    sum += v[u][i];
+                }
+                sum = group_sum<G>(sum);
+                const int t = t0 + u * kRows + row;
+                if (on[u]) {
+                    const float r = 1.0f / sum, l = m + logf(sum);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) acc[i] = fmaf(v[u][i], r, acc[i]);
+                    z = fmaf(l, l, z);
+                    ++n;
+                    if (j == 0) lse[t] = l;
+                } else if (t < b && j == 0) {
+                    lse[t] = 0.0f;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = expert_of<G, VEC>(i, j);
+            if (e < E) sm_red[row * E + e] = acc[i];
+        }
+        if (j == 0) { sm_z[row] = z; sm_n[row] = n; }
+        __syncthreads();
+        const int64_t cut = static_cast<int64_t>(blockIdx.x) + s;
+        for (int e = threadIdx.x; e < E; e += kBlThreads) {
+            float x = 0.0f;
+#pragma unroll 8
+            for (int r = 0; r < kRows; ++r) x += sm_red[r * E + e];
+            w.psum[cut * E + e] = x;
+            w.hist[cut * E + e] = sm_hist[e];
+        }
+        if (threadIdx.x == 0) {
+            float x = 0.0f;
+            int m = 0;
+            for (int r = 0; r < kRows; ++r) { x += sm_z[r]; m += sm_n[r]; }
+            w.zsum[cut] = x;
+            w.nval[cut] = m;
+        }
+        __syncthreads();
+    }
+}
+
+template <typename X>
+__device__ __forceinline__ X block_sum(X v, X* scratch) {
+    constexpr int kW = kRedCols * kRedRows / 32;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    X s = 0;
+#pragma unroll
+    for (int i = 0; i < kW; ++i) s += scratch[i];
+    return s;
+}
+
+// ---------------------------------------------------------------- forward, pass 2: the cuts of each sequence
+// Grid (column blocks, sequences). The last block to finish adds the blocks' shares of the losses in a fixed order.
+__global__ void __launch_bounds__(kRedCols * kRedRows)
+balance_reduce_kernel(const int32_t* __restrict__ offsets, int T, int E, int k, int S, int C, float alpha, float beta,
+                      BalWs w, float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ mean_prob,
+                      int32_t* valid, int* status) {
+    __shared__ float sm_p[kRedRows][kRedCols + 1];
+    __shared__ int sm_h[kRedRows][kRedCols + 1];
+    __shared__ double sm_d[kRedCols * kRedRows / 32];
+    __shared__ int sm_i[kRedCols * kRedRows / 32];
+    __shared__ bool sm_last;
+    const int col = threadIdx.x % kRedCols, r0 = threadIdx.x / kRedCols, s = blockIdx.y;
+    const int e = blockIdx.x * kRedCols + col;
+    wait_for_producer();
+    const int a = seq_start(offsets, s, T), b = seq_start(offsets, s + 1, T);
+    if (offsets && threadIdx.x == 0 && blockIdx.x == 0 && (offsets[s] != a || offsets[s + 1] != b || a > b))
+        set_status(status, kStatusCapacity);
+    const int lo = a / C, hi = b > a ? (b - 1) / C + 1 : lo;       // chunks that hold some of the sequence
+    float p = 0.0f;
+    int h = 0, n = 0;
+    double z = 0.0;
+    if (e < E) {
+#pragma unroll 4
+        for (int c = lo + r0; c < hi; c += kRedRows) {
+            p += w.psum[(static_cast<int64_t>(c) + s) * E + e];
+            h += w.hist[(static_cast<int64_t>(c) + s) * E + e];
+        }
+    }
+    for (int c = lo + threadIdx.x; c < hi; c += kRedCols * kRedRows) {
+        n += w.nval[c + s];
+        z += w.zsum[c + s];
+    }
+    sm_p[r0][col] = p;
+    sm_h[r0][col] = h;
+    n = block_sum(n, sm_i);
+    if (blockIdx.x == 0) z = block_sum(z, sm_d);
+    double share = 0.0;
+    if (r0 == 0 && e < E) {
+        double ps = 0.0;
+        int hs = 0;
+#pragma unroll
+        for (int r = 0; r < kRedRows; ++r) { ps += sm_p[r][col]; hs += sm_h[r][col]; }
+        const double mean = n > 0 ? ps / n : 0.0;
+        mean_prob[static_cast<int64_t>(s) * E + e] = static_cast<float>(mean);
+        counts[static_cast<int64_t>(s) * E + e] = hs;
+        share = n > 0 ? mean * hs * E / (static_cast<double>(k) * n) : 0.0;
+    }
+    share = block_sum(share, sm_d);
+    if (threadIdx.x == 0) {
+        w.part[static_cast<int64_t>(s) * gridDim.x + blockIdx.x] = share;
+        if (blockIdx.x == 0) { w.zpart[s] = z; valid[s] = n; }
+        __threadfence();
+        sm_last = atomicAdd(w.ticket, 1u) == gridDim.x * gridDim.y - 1;
+    }
+    __syncthreads();
+    if (!sm_last) return;
+    __threadfence();
+    double l0 = 0.0, l1 = 0.0;
+    int full = 0, total = 0;
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(S) * gridDim.x; i += kRedCols * kRedRows) l0 += __ldcg(w.part + i);
+    for (int i = threadIdx.x; i < S; i += kRedCols * kRedRows) {
+        const int v = __ldcg(valid + i);
+        l1 += __ldcg(w.zpart + i);
+        full += v > 0;
+        total += v;
+    }
+    l0 = block_sum(l0, sm_d);
+    l1 = block_sum(l1, sm_d);
+    full = block_sum(full, sm_i);
+    total = block_sum(total, sm_i);
+    if (threadIdx.x == 0) {
+        loss[0] = static_cast<float>(alpha * l0 / max(full, 1));
+        loss[1] = static_cast<float>(beta * l1 / max(total, 1));
+        valid[S] = full;
+        valid[S + 1] = total;
+    }
+}
+
+// ---------------------------------------------------------------- backward
+template <int G, int V, bool VEC, int U>
+__global__ void __launch_bounds__(kBlThreads)
+balance_backward_kernel(const float* __restrict__ logits, const float* __restrict__ lse,
+                        const int32_t* __restrict__ counts, const int32_t* __restrict__ valid,
+                        const uint8_t* __restrict__ mask, const int32_t* __restrict__ offsets, int T, int E, int k,
+                        int S, int C, float alpha, float beta, const float* __restrict__ dloss,
+                        float* __restrict__ dlogits) {
+    constexpr int kGroups = 32 / G, kRows = kBlWarps * kGroups;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % G;
+    const int row = warp * kGroups + lane / G;
+    const int c0 = blockIdx.x * C, c1 = min(c0 + C, T);
+    const float g0 = dloss ? dloss[0] : 1.0f, g1 = dloss ? dloss[1] : 1.0f;
+    const float zc = 2.0f * g1 * beta / static_cast<float>(max(valid[S + 1], 1));
+    for (int s = seq_behind(offsets, S, T, c0); s < S; ++s) {
+        const int a = max(seq_start(offsets, s, T), c0), b = min(seq_start(offsets, s + 1, T), c1);
+        if (a >= c1) break;
+        if (a >= b) continue;
+        const double n = max(valid[s], 1);
+        const float scale = static_cast<float>(static_cast<double>(g0) * alpha * E / (static_cast<double>(k) * n * n * max(valid[S], 1)));
+        float c[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = expert_of<G, VEC>(i, j);
+            c[i] = e < E ? scale * static_cast<float>(counts[static_cast<int64_t>(s) * E + e]) : 0.0f;
+        }
+        for (int t0 = a; t0 < b; t0 += kRows * U) {
+            float v[U][V], l[U];
+            bool on[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int t = t0 + u * kRows + row;
+                on[u] = t < b && (!mask || mask[t]);
+                const int64_t tt = on[u] ? t : a;
+                l[u] = lse[tt];
+                load_row<G, V, VEC>(logits + tt * E, E, j, -INFINITY, v[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                float dot = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    v[u][i] = expert_of<G, VEC>(i, j) < E ? expf(v[u][i] - l[u]) : 0.0f;
+                    dot = fmaf(v[u][i], c[i], dot);
+                }
+                dot = group_sum<G>(dot);
+                const int t = t0 + u * kRows + row;
+                if (t < b) {
+                    const float shift = fmaf(zc, l[u], -dot);
+                    float* out = dlogits + static_cast<int64_t>(t) * E;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[u][i] = on[u] ? v[u][i] * (c[i] + shift) : 0.0f;
+                    if constexpr (VEC) {
+#pragma unroll
+                        for (int q = 0; q < V / 4; ++q)
+                            if (4 * (j + G * q) < E)
+                                *reinterpret_cast<float4*>(out + 4 * (j + G * q)) =
+                                    make_float4(v[u][4 * q], v[u][4 * q + 1], v[u][4 * q + 2], v[u][4 * q + 3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < V; ++i)
+                            if (j + G * i < E) out[j + G * i] = v[u][i];
+                    }
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- launches
+// Calls f(tag) with the group size, values a lane and vector width for E experts.
+template <int G_, int V_, bool VEC_, int U_>
+struct RowForm { static constexpr int G = G_, V = V_, U = U_; static constexpr bool VEC = VEC_; };
+
+template <typename F>
+cudaError_t with_row_form(int E, F f) {
+    const bool vec = E % 4 == 0;
+    if (E <= 64) return vec ? f(RowForm<8, 8, true, 4>()) : f(RowForm<8, 8, false, 4>());
+    if (E <= 256) return vec ? f(RowForm<32, 8, true, 4>()) : f(RowForm<32, 8, false, 4>());
+    return vec ? f(RowForm<32, 16, true, 2>()) : f(RowForm<32, 16, false, 2>());
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool ptr_ok(const void* p) { return p != nullptr && aligned16(p); }
+
+moe_status_t check_balance(int T, int E, int k, int S, const void* offsets, float alpha, float beta) {
+    if (T < 0 || E <= 0 || k <= 0 || S <= 0 || !isfinite(alpha) || !isfinite(beta)) return MOE_ERR_INVALID_ARG;
+    if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (k > E || (!offsets && S != 1)) return MOE_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(T) * k >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_balance_workspace_size(int T, int E, int S) {
+    if (T < 0 || E <= 0 || E > MOE_MAX_EXPERTS || S <= 0 || S > MOE_MAX_SEQUENCES) return 0;
+    return carve_balance(T, E, S, nullptr).total;
+}
+
+moe_status_t moe_balance_loss(int T, int E, int k, const float* logits, const int32_t* topk_idx,
+                              const uint8_t* token_mask, const int32_t* seq_offsets, int S, float alpha, float beta,
+                              float* loss, int32_t* counts, float* mean_prob, float* lse, int32_t* seq_valid, void* ws,
+                              size_t ws_bytes, void* stream) {
+    moe_status_t st = check_balance(T, E, k, S, seq_offsets, alpha, beta);
+    if (st != MOE_OK) return st;
+    if (!ptr_ok(loss) || !ptr_ok(counts) || !ptr_ok(mean_prob) || !ptr_ok(seq_valid) || !ptr_ok(ws) ||
+        !aligned16(token_mask) || !aligned16(seq_offsets))
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!ptr_ok(logits) || !ptr_ok(topk_idx) || !ptr_ok(lse))) return MOE_ERR_INVALID_ARG;
+    const BalWs w = carve_balance(T, E, S, ws);
+    if (ws_bytes < w.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    int num_sms, *status;
+    if ((st = current_device(&num_sms, &status)) != MOE_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int C = chunk_tokens(T);
+    cudaError_t err;
+    if (T > 0) {
+        err = with_row_form(E, [&](auto f) {
+            using F = decltype(f);
+            balance_partial_kernel<F::G, F::V, F::VEC, F::U>
+                <<<chunks_of(T), kBlThreads, sizeof(float) * kBlWarps * (32 / F::G) * E, s>>>(
+                    logits, topk_idx, token_mask, seq_offsets, T, E, k, S, C, w, lse);
+            return cudaGetLastError();
+        });
+    } else {
+        err = cudaMemsetAsync(w.ticket, 0, sizeof(unsigned), s);   // no tokens: the reduction alone, over nothing
+    }
+    if (err != cudaSuccess) return MOE_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((E + kRedCols - 1) / kRedCols, S);
+    cfg.blockDim = dim3(kRedCols * kRedRows);
+    cfg.stream = s;
+    // the reduction may be set up while the partial sums run; it waits for them before it reads
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = T > 0 ? 1 : 0;
+    err = cudaLaunchKernelEx(&cfg, balance_reduce_kernel, seq_offsets, T, E, k, S, C, alpha, beta, w, loss, counts,
+                             mean_prob, seq_valid, status);
+    return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status_t moe_balance_loss_backward(int T, int E, int k, const float* logits, const float* lse,
+                                       const int32_t* counts, const int32_t* seq_valid, const uint8_t* token_mask,
+                                       const int32_t* seq_offsets, int S, float alpha, float beta, const float* dloss,
+                                       float* dlogits, void* stream) {
+    moe_status_t st = check_balance(T, E, k, S, seq_offsets, alpha, beta);
+    if (st != MOE_OK) return st;
+    if (!aligned16(token_mask) || !aligned16(seq_offsets) || !aligned16(dloss)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!ptr_ok(logits) || !ptr_ok(lse) || !ptr_ok(counts) || !ptr_ok(seq_valid) || !ptr_ok(dlogits)))
+        return MOE_ERR_INVALID_ARG;
+    int num_sms, *status;
+    if ((st = current_device(&num_sms, &status)) != MOE_OK) return st;
+    if (T == 0) return MOE_OK;
+    const cudaError_t err = with_row_form(E, [&](auto f) {
+        using F = decltype(f);
+        // a block's tokens: whole turns of its rows, several only where enough blocks are left to fill the GPU
+        const int turn = kBlWarps * (32 / F::G) * F::U;
+        const int C = std::max(std::max(kBwdTokens, turn), (T / (4 * num_sms) + turn - 1) / turn * turn);
+        balance_backward_kernel<F::G, F::V, F::VEC, F::U>
+            <<<(T + C - 1) / C, kBlThreads, 0, static_cast<cudaStream_t>(stream)>>>(
+                logits, lse, counts, seq_valid, token_mask, seq_offsets, T, E, k, S, C, alpha, beta, dloss, dlogits);
+        return cudaGetLastError();
+    });
+    return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,777 @@
+// Orthogonalised weight updates: X = G / (|G|_F + eps), then `steps` times
+//     A = X X^T,  B = b A + c A^2,  X <- a X + B X          (on the shorter side: X^T X where G is tall)
+// which drives X's singular values towards one value without a decomposition (Newton-Schulz iteration of the
+// matrix sign, in the quintic form), and O = scale X.
+//
+// All of it is matrix products, and the tensor cores bound it: with s <= l the sides, a step is s^2 l (A: half
+// of a symmetric product) + s^3 (A^2, half) + 2 s^2 l multiply-adds x 2. One persistent kernel of CTA pairs
+// runs every product of every step (256 x 256 tiles, tcgen05 cta_group::2, K blocks of 64 by TMA in a ring,
+// two accumulators in tensor memory). A tile waits on its own matrix's counter only, so the matrices of a
+// batch fill each other's dependencies and the tail of one product overlaps the head of the next; symmetric
+// products compute the tiles on and below the diagonal and store each twice, the second time transposed.
+//
+// Precision. Operands are fp16 (11 bits), sums fp32. The iteration multiplies X's small singular directions
+// by a, about 3.4, every step, and with them any rounding noise there: fp16 X alone ends up to 10 % off on
+// gradients of low rank. The noise grows only through the a X term, since B is near zero on those directions,
+// so X is carried as the sum of two fp16 values (22 bits): the first feeds the products, both enter a X in
+// the epilogue. That costs no tensor work and leaves the result closer than the rounding of O to bf16.
+// X is stored times a power of two near sqrt(l) (entries near 1), A and B times 64.
+#include <cmath>
+
+#include <algorithm>
+
+#include <cuda_fp16.h>
+
+#include "../../include/moe_fp8.h"
+#include "common.cuh"
+
+namespace moe {
+
+moe_status_t current_device(int* num_sms, int** status);
+
+namespace {
+
+constexpr uint64_t kOrthoWaitNs = 4000000000ull;
+constexpr int kOT = 256;                     // tile edge of a CTA pair
+constexpr int kOK = 64;                      // K values a stage holds: 128 bytes
+constexpr int kOStages = 5;
+constexpr int kOBox = 64 * kOK * 2;          // one 64 x 64 box of an operand: 8 KB
+constexpr int kOOper = 2 * kOBox;            // a CTA's 128 rows of an operand
+constexpr int kOThreads = 384;               // TMA, MMA, two idle warps, eight epilogue warps
+constexpr int kOEpi = 8;
+constexpr float kPScale = 64.0f;             // A and B are stored times this
+constexpr int kMaxSteps = 32;
+
+struct SmemO {
+    uint8_t a[kOStages][kOOper];
+    uint8_t b[kOStages][kOOper];
+    uint8_t stage[kOEpi][2][4096];           // per epilogue warp: 32 rows x 64 columns of 16-bit values, twice
+    uint64_t full[kOStages];
+    uint64_t empty[kOStages];
+    uint64_t tfull[2];
+    uint64_t tempty[2];
+    uint64_t eload[kOEpi];
+    uint32_t tmem_base;
+    volatile int abort_flag;
+};
+
+// Tensor maps over a wave's buffers, [matrices][rows][columns] of fp16: operand boxes of 64 x 64 values,
+// epilogue boxes of 64 columns x 32 rows and, for transposed stores, 32 columns x 64 rows.
+struct OrthoMaps {
+    CUtensorMap hi_op[2], hi_ep[2], lo_ep;
+    CUtensorMap p_op, p_ep, p_tr;            // 64 A
+    CUtensorMap q_op, q_ep, q_tr;            // 64 B
+};
+
+struct OrthoArgs {
+    int M, N;                // rows and columns of a matrix
+    int mats;                // matrices of the wave
+    int steps;
+    int interleaved;
+    float a, b, c;
+    float out_scale;         // scale / the power of two X is stored with
+    float gram_scale;        // 64 / that power squared
+    uint16_t* O;             // the wave's first matrix
+    unsigned* done;          // [mats] finished warps of tiles
+    int* status;
+};
+
+// One tile of one product: matrix b, product 0 = A, 1 = B, 2 = the update, of step `step`.
+struct OrthoTile {
+    int step, prod, b, ti, tj;
+};
+
+struct OrthoShape {
+    int s, l, nb, rb, cb, ns, nu;     // sides, tiles: symmetric per side, update rows / columns, per product
+    bool tall;
+    __device__ OrthoShape(const OrthoArgs& g) {
+        tall = g.M > g.N;
+        s = min(g.M, g.N);
+        l = max(g.M, g.N);
+        nb = (s + kOT - 1) / kOT;
+        ns = nb * (nb + 1) / 2;
+        rb = (g.M + kOT - 1) / kOT;
+        cb = (g.N + kOT - 1) / kOT;
+        nu = rb * cb;
+    }
+};
+
+// Walks this cluster's tiles: products in order, each over all matrices, every `stride`-th tile.
+struct OrthoWalk {
+    const OrthoArgs& g;
+    const OrthoShape& sh;
+    int pos, step, prod, stride;
+    __device__ OrthoWalk(const OrthoArgs& g_, const OrthoShape& sh_, int first, int stride_)
+        : g(g_), sh(sh_), pos(first), step(0), prod(0), stride(stride_) {
+        settle();
+    }
+    __device__ int per_matrix() const { return prod == 2 ? sh.nu : sh.ns; }
+    __device__ void settle() {
+        while (step < g.steps && pos >= g.mats * per_matrix()) {
+            pos -= g.mats * per_matrix();
+            if (++prod == 3) { prod = 0; ++step; }
+        }
+    }
+    __device__ bool more() const { return step < g.steps; }
+    __device__ void next() { pos += stride; settle(); }
+    __device__ OrthoTile tile() const {
+        OrthoTile t;
+        t.step = step;
+        t.prod = prod;
+        t.b = pos / per_matrix();
+        const int i = pos - t.b * per_matrix();
+        if (prod == 2) {
+            // the shorter side runs fastest: neighbours share the longer operand's panel
+            if (sh.tall) { t.ti = i / sh.cb; t.tj = i - t.ti * sh.cb; }
+            else { t.tj = i / sh.rb; t.ti = i - t.tj * sh.rb; }
+        } else {
+            int r = static_cast<int>((sqrtf(8.0f * i + 1.0f) - 1.0f) * 0.5f);
+            while ((r + 1) * (r + 2) / 2 <= i) ++r;
+            while (r * (r + 1) / 2 > i) --r;
+            t.ti = r;
+            t.tj = i - r * (r + 1) / 2;
+        }
+        return t;
+    }
+    // Finished warps of tiles its matrix needs before this tile may start: all earlier products'.
+    __device__ unsigned needs() const {
+        const int tiles = step * (2 * sh.ns + sh.nu) + prod * sh.ns;
+        return static_cast<unsigned>(tiles) * (2 * kOEpi);
+    }
+};
+
+__device__ __forceinline__ uint32_t pack_half2(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_half2(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Row r of matrix m in the caller's array (interleaved: blocks of 128 rows of two matrices in turn).
+__device__ __forceinline__ int64_t user_row(int m, int r, int M, int interleaved) {
+    if (!interleaved) return static_cast<int64_t>(m) * M + r;
+    return static_cast<int64_t>(m >> 1) * 2 * M + (r / kGroup * 2 + (m & 1)) * kGroup + r % kGroup;
+}
+
+__global__ void __launch_bounds__(kOThreads, 1)
+ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant__ OrthoArgs g) {
+    extern __shared__ uint8_t smem_raw[];
+    SmemO& sm = *reinterpret_cast<SmemO*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const OrthoShape sh(g);
+    OrthoWalk w(g, sh, static_cast<int>(cluster_id_x()), static_cast<int>(cluster_count_x()));
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kOStages; ++s) {
+            mbar_init(&sm.full[s], 1);       // the leader arms it with both CTAs' bytes
+            mbar_init(&sm.empty[s], 1);      // the commit of the stage's MMAs reaches both CTAs
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sm.tfull[i], 1);
+            mbar_init(&sm.tempty[i], 2 * kOEpi);
+        }
+        for (int i = 0; i < kOEpi; ++i) mbar_init(&sm.eload[i], 1);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&sm.tmem_base, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+
+    auto fail = [&]() {
+        set_status(g.status, kStatusTimeout);
+        sm.abort_flag = 1;
+        st_shared_cluster_u32(mapa_shared(smem_u32((const void*)&sm.abort_flag), rank ^ 1u), 1u);
+    };
+    // Waits until matrix b's counter reaches `need`, then lets later TMA accesses see what was stored before it.
+    auto wait_for = [&](int b, unsigned need) -> bool {
+        if (load_acquire_gpu(g.done + b) < need) {
+            const uint64_t t0 = globaltimer_ns();
+            while (load_acquire_gpu(g.done + b) < need) {
+                if (sm.abort_flag || globaltimer_ns() - t0 > kOrthoWaitNs) return false;
+                __nanosleep(64);
+            }
+        }
+        fence_proxy_async();
+        return true;
+    };
+
+    if (warp == 0) {
+        // ---------------- producer: this CTA's 128 rows of the A operand and its half of the B operand
+        if (lane == 0) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (; ok && w.more(); w.next()) {
+                const OrthoTile t = w.tile();
+                if (!wait_for(t.b, w.needs())) { fail(); break; }
+                const int cur = t.step & 1;
+                // product 0: X X^T (X^T X); 1: A A; 2: B X (X B)
+                const CUtensorMap* ma = t.prod == 0 ? &maps.hi_op[cur] : t.prod == 1 ? &maps.p_op : sh.tall ? &maps.hi_op[cur] : &maps.q_op;
+                const CUtensorMap* mb = t.prod == 0 ? &maps.hi_op[cur] : t.prod == 1 ? &maps.p_op : sh.tall ? &maps.q_op : &maps.hi_op[cur];
+                const bool a_mn = t.prod == 0 && sh.tall;
+                const bool b_mn = (t.prod == 0 && sh.tall) || (t.prod == 2 && !sh.tall);
+                const int K = t.prod == 0 ? sh.l : sh.s;
+                const int ra = t.ti * kOT + static_cast<int>(rank) * 128, rb = t.tj * kOT + static_cast<int>(rank) * 128;
+                for (int k0 = 0; k0 < K; k0 += kOK, ++it) {
+                    const int s = it % kOStages;
+                    if (!mbar_wait(&sm.empty[s], ((it / kOStages) & 1) ^ 1, kOrthoWaitNs)) { fail(); ok = false; break; }
+                    const uint32_t fb = mapa_shared(smem_u32(&sm.full[s]), 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 4 * kOOper);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int ya = ra + 64 * i, yb = rb + 64 * i;
+                        tma_load_3d_pair(sm.a[s] + i * kOBox, ma, fb, a_mn ? ya : k0, a_mn ? k0 : ya, t.b);
+                        tma_load_3d_pair(sm.b[s] + i * kOBox, mb, fb, b_mn ? yb : k0, b_mn ? k0 : yb, t.b);
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer: the leader, for both CTAs
+        if (lane == 0 && rank == 0) {
+            uint32_t it = 0, ti = 0;
+            bool ok = true;
+            for (; ok && w.more() && !sm.abort_flag; w.next(), ++ti) {
+                const OrthoTile t = w.tile();
+                const bool a_mn = t.prod == 0 && sh.tall;
+                const bool b_mn = (t.prod == 0 && sh.tall) || (t.prod == 2 && !sh.tall);
+                const int K = t.prod == 0 ? sh.l : sh.s;
+                const uint32_t idesc = f16_idesc(2 * 128, kOT, false, a_mn, b_mn);
+                const uint32_t buf = ti & 1, d = tmem + buf * kOT;
+                if (!mbar_wait(&sm.tempty[buf], ((ti >> 1) & 1) ^ 1, kOrthoWaitNs)) { fail(); break; }
+                tc_fence_after();
+                for (int k0 = 0; k0 < K; k0 += kOK, ++it) {
+                    const int s = it % kOStages;
+                    if (!mbar_wait(&sm.full[s], (it / kOStages) & 1, kOrthoWaitNs)) { fail(); ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(sm.a[s]), b0 = smem_u32(sm.b[s]);
+#pragma unroll
+                    for (int kk = 0; kk < kOK / 16; ++kk) {
+                        // 16 K values: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major box
+                        const uint64_t da = a_mn ? sw128_mnmajor_desc(a0 + kk * 2048, kOBox) : sw128_kmajor_desc(a0 + kk * 32);
+                        const uint64_t db = b_mn ? sw128_mnmajor_desc(b0 + kk * 2048, kOBox) : sw128_kmajor_desc(b0 + kk * 32);
+                        umma_f16_pair(d, da, db, idesc, k0 + kk > 0);
+                    }
+                    umma_commit_pair(&sm.empty[s], 0x3);
+                }
+                if (ok) umma_commit_pair(&sm.tfull[buf], 0x3);
+            }
+        }
+    } else if (warp >= 4) {
+        // ---------------- epilogue: warp = lane quadrant q x column half; 64 columns at a time through its stage
+        const int ew = warp - 4, q = warp & 3, half = ew >> 2;
+        const uint32_t st0 = smem_u32(sm.stage[ew][0]), st1 = smem_u32(sm.stage[ew][1]);
+        const uint32_t tempty0 = mapa_shared(smem_u32(&sm.tempty[0]), 0);
+        uint32_t ti = 0, loads = 0;
+        bool ok = true;
+        for (; ok && w.more(); w.next(), ++ti) {
+            if (sm.abort_flag) break;
+            const OrthoTile t = w.tile();
+            const uint32_t buf = ti & 1;
+            const int row0 = t.ti * kOT + static_cast<int>(rank) * 128 + q * 32;
+            const int rows = t.prod == 2 ? g.M : sh.s, cols = t.prod == 2 ? g.N : sh.s;
+            const int cur = t.step & 1;
+            const bool last = t.prod == 2 && t.step == g.steps - 1;
+            const bool mirror = t.prod != 2 && t.ti != t.tj;
+#pragma unroll 1
+            for (int sub = 0; sub < 2; ++sub) {
+                const int col0 = t.tj * kOT + half * 128 + sub * 64;
+                // the stage is free once the last stores have read it; then the tile's own values come in
+                int good = 1;
+                if (lane == 0) {
+                    bulk_wait_read_all();
+                    if (t.prod != 0) {
+                        if (sub == 0) good = wait_for(t.b, w.needs());
+                        if (good) {
+                            mbar_arrive_expect_tx(&sm.eload[ew], t.prod == 1 ? 4096 : 8192);
+                            if (t.prod == 1) {
+                                tma_load_3d(sm.stage[ew][0], &maps.p_ep, &sm.eload[ew], col0, row0, t.b);
+                            } else {
+                                tma_load_3d(sm.stage[ew][0], &maps.hi_ep[cur], &sm.eload[ew], col0, row0, t.b);
+                                tma_load_3d(sm.stage[ew][1], &maps.lo_ep, &sm.eload[ew], col0, row0, t.b);
+                            }
+                        }
+                    }
+                }
+                if (!__shfl_sync(0xffffffffu, good, 0)) { fail(); ok = false; break; }
+                if (sub == 0) {
+                    if (!mbar_wait(&sm.tfull[buf], (ti >> 1) & 1, kOrthoWaitNs)) { fail(); ok = false; break; }
+                    tc_fence_after();
+                }
+                if (t.prod != 0) {
+                    if (!mbar_wait(&sm.eload[ew], loads & 1, kOrthoWaitNs)) { fail(); ok = false; break; }
+                    ++loads;
+                }
+                const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kOT + half * 128 + sub * 64;
+                float v[2][32];
+                tmem_ld32(taddr, v[0]);
+                tmem_ld32(taddr + 32, v[1]);
+                tmem_ld_wait();
+                if (sub == 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (rank) mbar_arrive_cluster(tempty0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
+                        else mbar_arrive(&sm.tempty[buf]);
+                    }
+                }
+                // 16-byte piece p (8 columns) of row `lane` sits at p ^ (lane & 7) (128-byte swizzle)
+#pragma unroll
+                for (int p = 0; p < 8; ++p) {
+                    const uint32_t at = static_cast<uint32_t>(lane * 128 + ((p ^ (lane & 7)) << 4));
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = v[p >> 2][(p & 3) * 8 + i];
+                    if (t.prod == 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] *= g.gram_scale;
+                    } else if (t.prod == 1) {
+                        const uint4 u = ld_shared_v4(st0 + at);
+                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 f = unpack_half2(uu[i]);
+                            x[2 * i] = fmaf(g.b, f.x, g.c * (1.0f / kPScale) * x[2 * i]);
+                            x[2 * i + 1] = fmaf(g.b, f.y, g.c * (1.0f / kPScale) * x[2 * i + 1]);
+                        }
+                    } else {
+                        const uint4 u = ld_shared_v4(st0 + at), r = ld_shared_v4(st1 + at);
+                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 h = unpack_half2(uu[i]), lo = unpack_half2(rr[i]);
+                            x[2 * i] = fmaf(g.a, h.x + lo.x, (1.0f / kPScale) * x[2 * i]);
+                            x[2 * i + 1] = fmaf(g.a, h.y + lo.y, (1.0f / kPScale) * x[2 * i + 1]);
+                        }
+                    }
+                    uint32_t o[4];
+                    if (last) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(g.out_scale * x[2 * i], g.out_scale * x[2 * i + 1]);
+                            o[i] = *reinterpret_cast<const uint32_t*>(&b2);
+                        }
+                        st_shared_v4(st0 + at, o[0], o[1], o[2], o[3]);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) o[i] = pack_half2(x[2 * i], x[2 * i + 1]);
+                        st_shared_v4(st0 + at, o[0], o[1], o[2], o[3]);
+                        if (t.prod == 2) {
+                            uint32_t r[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 h = unpack_half2(o[i]);
+                                r[i] = pack_half2(x[2 * i] - h.x, x[2 * i + 1] - h.y);
+                            }
+                            st_shared_v4(st1 + at, r[0], r[1], r[2], r[3]);
+                        } else if (mirror) {
+                            // the transposed box: row j (a column here) of 32 values, 64-byte swizzle
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int j = p * 8 + i;
+                                const uint32_t to = st1 + j * 64 + ((((lane >> 3) ^ (j >> 1)) & 3) << 4) + (lane & 7) * 2;
+                                const uint16_t h = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+                                asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(h) : "memory");
+                            }
+                        }
+                    }
+                }
+                if (last) {
+                    // rows leave 16 bytes a lane, eight lanes a row; sizes that are no multiple of 8 value by value
+                    __syncwarp();
+                    const bool vec = g.N % 8 == 0;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = i * 4 + (lane >> 3), p = lane & 7;
+                        const int grow = row0 + r, gcol = col0 + p * 8;
+                        if (grow < rows && gcol < cols) {
+                            const uint4 u = ld_shared_v4(st0 + r * 128 + ((p ^ (r & 7)) << 4));
+                            uint16_t* dst = g.O + user_row(t.b, grow, g.M, g.interleaved) * g.N + gcol;
+                            if (vec) {
+                                *reinterpret_cast<uint4*>(dst) = u;
+                            } else {
+                                const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                                for (int c = 0; c < 8; ++c)
+                                    if (gcol + c < cols) dst[c] = static_cast<uint16_t>(uu[c >> 1] >> (16 * (c & 1)));
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                } else {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (row0 < rows && col0 < cols) {
+                            const CUtensorMap* m = t.prod == 0 ? &maps.p_ep : t.prod == 1 ? &maps.q_ep : &maps.hi_ep[cur ^ 1];
+                            tma_store_3d(m, sm.stage[ew][0], col0, row0, t.b);
+                            if (t.prod == 2) tma_store_3d(&maps.lo_ep, sm.stage[ew][1], col0, row0, t.b);
+                            if (mirror) tma_store_3d(t.prod == 0 ? &maps.p_tr : &maps.q_tr, sm.stage[ew][1], row0, col0, t.b);
+                        }
+                        bulk_commit();
+                    }
+                }
+            }
+            if (ok && !last && lane == 0) {
+                // this warp's part of the tile is in memory: count it
+                bulk_wait_all();
+                fence_proxy_async();
+                add_release_gpu(g.done + t.b, 1);
+            }
+        }
+    }
+
+    if (warp >= 4 && lane == 0) bulk_wait_all();
+    tc_fence_before();
+    cluster_sync();      // neither CTA leaves while the leader's MMAs may read the other's shared memory
+    if (sm.abort_flag) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000) __nanosleep(1000);   // copies and MMAs in flight land
+    }
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- the norm, and X in two fp16 parts
+constexpr int kNormThreads = 256, kNormVals = 8;     // values a thread takes at a time
+constexpr int kNormBlocks = 296;
+
+int norm_blocks(int64_t n) {
+    return static_cast<int>(std::min<int64_t>(kNormBlocks, (n + kNormThreads * kNormVals - 1) / (kNormThreads * kNormVals)));
+}
+
+// Place in the caller's array of value e of the wave's matrix m (offset from the wave's first matrix).
+__device__ __forceinline__ int64_t user_at(int64_t e, int m, int M, int N, int interleaved) {
+    if (!interleaved) return static_cast<int64_t>(m) * M * N + e;
+    const int64_t slab = static_cast<int64_t>(kGroup) * N;
+    return static_cast<int64_t>(m >> 1) * 2 * M * N + (e / slab * 2 + (m & 1)) * slab + e % slab;
+}
+
+// Values e .. e + 7 of matrix m (n in all); VEC: aligned and whole.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load_vals(const void* G, int64_t e, int64_t n, int m, int M, int N, int interleaved,
+                                          float (&v)[kNormVals]) {
+    if constexpr (VEC) {
+        const int64_t at = user_at(e, m, M, N, interleaved);
+        if constexpr (F32) {
+            const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(G) + at);
+            const float4 x = p[0], y = p[1];
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+        } else {
+            const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(G) + at);
+            const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(uu[i] << 16);
+                v[2 * i + 1] = __uint_as_float(uu[i] & 0xffff0000u);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kNormVals; ++i) {
+            v[i] = 0.0f;
+            if (e + i < n) {
+                const int64_t at = user_at(e + i, m, M, N, interleaved);
+                v[i] = F32 ? static_cast<const float*>(G)[at] : bf16_bits_to_f32(static_cast<const uint16_t*>(G)[at]);
+            }
+        }
+    }
+}
+
+__device__ __forceinline__ double block_sum_f64(double v, double* scratch) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    __syncthreads();
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < kNormThreads / 32; ++i) s += scratch[i];
+    return s;
+}
+
+// Sums of squares in fp64 (fp32 would overflow from 2^64 on and lose small gradients below 2^-63).
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(kNormThreads)
+ortho_norm_kernel(const void* __restrict__ G, int M, int N, int interleaved, double* __restrict__ part,
+                  unsigned* __restrict__ done) {
+    __shared__ double scratch[kNormThreads / 32];
+    const int m = blockIdx.y;
+    const int64_t n = static_cast<int64_t>(M) * N;
+    if (blockIdx.x == 0 && threadIdx.x == 0) done[m] = 0;
+    double s = 0.0;
+    for (int64_t e = (static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x) * kNormVals; e < n;
+         e += static_cast<int64_t>(gridDim.x) * kNormThreads * kNormVals) {
+        float v[kNormVals];
+        load_vals<F32, VEC>(G, e, n, m, M, N, interleaved, v);
+#pragma unroll
+        for (int i = 0; i < kNormVals; ++i) s = fma(static_cast<double>(v[i]), static_cast<double>(v[i]), s);
+    }
+    s = block_sum_f64(s, scratch);
+    if (threadIdx.x == 0) part[static_cast<int64_t>(m) * gridDim.x + blockIdx.x] = s;
+}
+
+template <bool F32, bool VEC>
+__global__ void __launch_bounds__(kNormThreads)
+ortho_convert_kernel(const void* __restrict__ G, int M, int N, int ldx, int interleaved, const double* __restrict__ part,
+                     double eps, double xscale, uint16_t* __restrict__ hi, uint16_t* __restrict__ lo) {
+    __shared__ double scratch[kNormThreads / 32];
+    const int m = blockIdx.y;
+    const int64_t n = static_cast<int64_t>(M) * N;
+    double s = 0.0;
+    for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kNormThreads) s += part[static_cast<int64_t>(m) * gridDim.x + i];
+    s = block_sum_f64(s, scratch);
+    const double inv = xscale / (sqrt(s) + eps);
+    const int64_t base = static_cast<int64_t>(m) * M * ldx;
+    for (int64_t e = (static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x) * kNormVals; e < n;
+         e += static_cast<int64_t>(gridDim.x) * kNormThreads * kNormVals) {
+        float v[kNormVals];
+        load_vals<F32, VEC>(G, e, n, m, M, N, interleaved, v);
+        alignas(16) uint16_t h[kNormVals], r[kNormVals];
+#pragma unroll
+        for (int i = 0; i < kNormVals; ++i) {
+            // in fp64: 1 / norm of a tiny gradient is outside fp32
+            const float x = static_cast<float>(v[i] * inv);
+            const __half a = __float2half_rn(x);
+            h[i] = __half_as_ushort(a);
+            r[i] = __half_as_ushort(__float2half_rn(x - __half2float(a)));
+        }
+        if constexpr (VEC) {
+            *reinterpret_cast<uint4*>(hi + base + e) = *reinterpret_cast<const uint4*>(h);
+            *reinterpret_cast<uint4*>(lo + base + e) = *reinterpret_cast<const uint4*>(r);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kNormVals; ++i)
+                if (e + i < n) {
+                    const int64_t at = base + (e + i) / N * ldx + (e + i) % N;
+                    hi[at] = h[i];
+                    lo[at] = r[i];
+                }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- workspace and launches
+// A wave holds enough matrices to give every CTA pair a tile of the symmetric products, twice over, and never
+// fewer than two (one fills the other's waits); a batch is cut into equal waves that use the workspace in turn.
+int wave_of(int mats, int M, int N, int interleaved) {
+    const int nb = (std::min(M, N) + kOT - 1) / kOT, ns = nb * (nb + 1) / 2;
+    const int most = std::max(2, (148 + ns - 1) / ns);
+    const int waves = (mats + most - 1) / most;
+    int w = (mats + waves - 1) / waves;
+    if (interleaved) w = (w + 1) / 2 * 2;            // a wave starts at a first matrix
+    return w;
+}
+
+struct OrthoWs {
+    uint16_t* hi[2];
+    uint16_t* lo;
+    uint16_t* p;
+    uint16_t* q;
+    double* part;
+    unsigned* done;
+    size_t total;
+};
+
+OrthoWs carve_ortho(int wave, int M, int N, void* base) {
+    OrthoWs w;
+    const size_t ldx = (N + 7) / 8 * 8, s = std::min(M, N), lds = (s + 7) / 8 * 8;
+    uint8_t* p = static_cast<uint8_t*>(base);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t* r = p ? p + off : nullptr;
+        off += (bytes + 255) / 256 * 256;
+        return r;
+    };
+    for (auto& h : w.hi) h = reinterpret_cast<uint16_t*>(take(2 * wave * M * ldx));
+    w.lo = reinterpret_cast<uint16_t*>(take(2 * wave * M * ldx));
+    w.p = reinterpret_cast<uint16_t*>(take(2 * wave * s * lds));
+    w.q = reinterpret_cast<uint16_t*>(take(2 * wave * s * lds));
+    w.part = reinterpret_cast<double*>(take(8ull * wave * kNormBlocks));
+    w.done = reinterpret_cast<unsigned*>(take(4ull * wave));
+    w.total = off;
+    return w;
+}
+
+// [mats][rows][cols] of fp16, rows ld values apart, in boxes of bx columns x by rows.
+bool make_half_map(CUtensorMap* m, const void* base, int mats, int rows, int cols, int bx, int by) {
+    EncodeTiledFn fn = tensor_map_encoder();
+    if (!fn) return false;
+    const cuuint64_t ld = (cols + 7) / 8 * 8;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(mats)};
+    const cuuint64_t strides[2] = {2 * ld, 2 * ld * static_cast<cuuint64_t>(rows)};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(bx), static_cast<cuuint32_t>(by), 1};
+    const cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, bx == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+moe_status_t check_ortho(int batch, int M, int N, int interleaved) {
+    if (batch < 0 || M <= 0 || N <= 0 || (interleaved != 0 && interleaved != 1)) return MOE_ERR_INVALID_ARG;
+    if (M > 16384 || N > 16384 || batch > 16384) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (interleaved && M % kGroup) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return MOE_OK;
+}
+
+// Whether every X and B of the iteration stays inside what fp16 holds: bounds the largest singular value after
+// each step from that before it (|a x + b x^3 + c x^5| over [0, r] has its maximum at r or where the derivative
+// is zero), and |b x^2 + c x^4| likewise.
+bool coefficients_ok(int steps, float a, float b, float c) {
+    if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
+    const double A = a, B = b, C = c;
+    double r2 = 1.0;                                   // the largest singular value, squared
+    for (int i = 0; i < steps; ++i) {
+        auto poly = [&](double u) { return std::abs(A + B * u + C * u * u) * std::sqrt(u); };
+        auto gram = [&](double u) { return std::abs(B * u + C * u * u); };
+        double top = poly(r2), bmax = gram(r2);
+        const double disc = 9.0 * B * B - 20.0 * A * C;
+        if (C != 0.0 && disc >= 0.0)
+            for (double sgn : {-1.0, 1.0}) {
+                const double u = (-3.0 * B + sgn * std::sqrt(disc)) / (10.0 * C);
+                if (u > 0.0 && u < r2) top = std::max(top, poly(u));
+            }
+        if (C == 0.0 && B != 0.0 && -A / (3.0 * B) > 0.0 && -A / (3.0 * B) < r2) top = std::max(top, poly(-A / (3.0 * B)));
+        if (C != 0.0 && -B / (2.0 * C) > 0.0 && -B / (2.0 * C) < r2) bmax = std::max(bmax, gram(-B / (2.0 * C)));
+        if (!(top <= 8.0) || !(bmax <= 256.0)) return false;
+        r2 = std::max(top * top, 1e-30);
+    }
+    return true;
+}
+
+template <bool F32>
+cudaError_t launch_prepare(const void* G, int mats, const OrthoArgs& g, const OrthoWs& w, double eps, double xscale,
+                           cudaStream_t s) {
+    const dim3 grid(norm_blocks(static_cast<int64_t>(g.M) * g.N), mats);
+    const int ldx = (g.N + 7) / 8 * 8;
+    if (g.N % 8 == 0) {
+        ortho_norm_kernel<F32, true><<<grid, kNormThreads, 0, s>>>(G, g.M, g.N, g.interleaved, w.part, w.done);
+        ortho_convert_kernel<F32, true><<<grid, kNormThreads, 0, s>>>(G, g.M, g.N, ldx, g.interleaved, w.part, eps, xscale, w.hi[0], w.lo);
+    } else {
+        ortho_norm_kernel<F32, false><<<grid, kNormThreads, 0, s>>>(G, g.M, g.N, g.interleaved, w.part, w.done);
+        ortho_convert_kernel<F32, false><<<grid, kNormThreads, 0, s>>>(G, g.M, g.N, ldx, g.interleaved, w.part, eps, xscale, w.hi[0], w.lo);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t launch_steps(const OrthoMaps& maps, const OrthoArgs& g, int num_sms, cudaStream_t s) {
+    const size_t smem = sizeof(SmemO) + 1024;
+    cudaError_t err = cudaFuncSetAttribute(ortho_steps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeCooperative;      // blocks wait on one another: all of them or none
+    attr[1].val.cooperative = 1;
+    cfg.blockDim = dim3(kOThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    static int clusters[64] = {0};
+    int dev = 0;
+    if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    int n = __atomic_load_n(&clusters[dev], __ATOMIC_RELAXED);
+    if (n == 0) {
+        cfg.gridDim = dim3(2 * (num_sms / 2));
+        if ((err = cudaOccupancyMaxActiveClusters(&n, ortho_steps_kernel, &cfg)) != cudaSuccess) return err;
+        if (n <= 0) return cudaErrorInvalidConfiguration;
+        __atomic_store_n(&clusters[dev], n, __ATOMIC_RELAXED);
+    }
+    cfg.gridDim = dim3(2 * n);
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, ortho_steps_kernel, maps, g);
+}
+
+bool ptr_ok(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+size_t moe_orthogonalise_workspace_size(int batch, int M, int N, int interleaved) {
+    if (check_ortho(batch, M, N, interleaved) != MOE_OK || batch == 0) return 0;
+    return carve_ortho(wave_of(batch * (interleaved ? 2 : 1), M, N, interleaved), M, N, nullptr).total;
+}
+
+moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const void* G, int g_type, int steps, float a,
+                               float b, float c, float eps, float scale, void* O, void* ws, size_t ws_bytes,
+                               void* stream) {
+    moe_status_t st = check_ortho(batch, M, N, interleaved);
+    if (st != MOE_OK) return st;
+    if (g_type != MOE_TYPE_BF16 && g_type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
+    if (steps <= 0 || steps > kMaxSteps || !coefficients_ok(steps, a, b, c)) return MOE_ERR_INVALID_ARG;
+    if (!std::isfinite(eps) || eps < 0.0f || !std::isfinite(scale)) return MOE_ERR_INVALID_ARG;
+    if (batch == 0) return MOE_OK;
+    if (!ptr_ok(G) || !ptr_ok(O) || !ptr_ok(ws) || (reinterpret_cast<uintptr_t>(ws) & 255)) return MOE_ERR_INVALID_ARG;
+    const int mats = batch * (interleaved ? 2 : 1), wave = wave_of(mats, M, N, interleaved);
+    const OrthoWs w = carve_ortho(wave, M, N, ws);
+    if (ws_bytes < w.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    int num_sms, *status;
+    if ((st = current_device(&num_sms, &status)) != MOE_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const double xscale = std::exp2(std::floor(0.5 * std::log2(static_cast<double>(std::max(M, N))) + 0.5));
+    const size_t size = g_type == MOE_TYPE_FP32 ? 4 : 2;
+    const int side = std::min(M, N);
+    for (int m0 = 0; m0 < mats; m0 += wave) {
+        OrthoArgs g;
+        g.M = M;
+        g.N = N;
+        g.mats = std::min(wave, mats - m0);
+        g.steps = steps;
+        g.interleaved = interleaved;
+        g.a = a;
+        g.b = b;
+        g.c = c;
+        g.out_scale = static_cast<float>(scale / xscale);
+        g.gram_scale = static_cast<float>(kPScale / (xscale * xscale));
+        const size_t first = static_cast<size_t>(m0) * M * N;
+        g.O = static_cast<uint16_t*>(O) + first;
+        g.done = w.done;
+        g.status = status;
+        const void* gw = static_cast<const uint8_t*>(G) + first * size;
+        OrthoMaps maps;
+        bool ok = true;
+        for (int i = 0; i < 2; ++i) {
+            ok = ok && make_half_map(&maps.hi_op[i], w.hi[i], g.mats, M, N, 64, 64);
+            ok = ok && make_half_map(&maps.hi_ep[i], w.hi[i], g.mats, M, N, 64, 32);
+        }
+        ok = ok && make_half_map(&maps.lo_ep, w.lo, g.mats, M, N, 64, 32);
+        ok = ok && make_half_map(&maps.p_op, w.p, g.mats, side, side, 64, 64);
+        ok = ok && make_half_map(&maps.p_ep, w.p, g.mats, side, side, 64, 32);
+        ok = ok && make_half_map(&maps.p_tr, w.p, g.mats, side, side, 32, 64);
+        ok = ok && make_half_map(&maps.q_op, w.q, g.mats, side, side, 64, 64);
+        ok = ok && make_half_map(&maps.q_ep, w.q, g.mats, side, side, 64, 32);
+        ok = ok && make_half_map(&maps.q_tr, w.q, g.mats, side, side, 32, 64);
+        if (!ok) return MOE_ERR_CUDA;
+        cudaError_t err = g_type == MOE_TYPE_FP32 ? launch_prepare<true>(gw, g.mats, g, w, eps, xscale, s)
+                                                  : launch_prepare<false>(gw, g.mats, g, w, eps, xscale, s);
+        if (err == cudaSuccess) err = launch_steps(maps, g, num_sms, s);
+        if (err != cudaSuccess) return MOE_ERR_CUDA;
+    }
+    return MOE_OK;
+}
+
+}  // extern "C"

@@ -16,7 +16,10 @@
  *   moe_combine          weighted un-permute y = sum_j w_j * o_j
  *   moe_forward          all of the above on one stream, no host sync
  * and, for training, moe_balance_bias: the auxiliary-loss-free update of the
- * routing bias b from the per-expert counts moe_permute reports; and
+ * routing bias b from the per-expert counts moe_permute reports;
+ * moe_balance_loss, moe_balance_loss_backward and moe_router_backward: the
+ * balance loss on the router's logits and its way back to W_g, b and x;
+ * moe_orthogonalise: the orthogonalised update of the experts' matrices; and
  * moe_grouped_gemm_w4: the grouped GEMM with 4-bit expert weights (masked
  * layout).
  *
@@ -65,11 +68,13 @@ typedef enum { MOE_CONTIG_AUTO = 0, MOE_CONTIG_SINGLE = 1, MOE_CONTIG_PAIR = 2 }
 /* Expert weights: E4M3 with one fp32 scale per 128x128 block, or 4-bit levels with one fp32 scale per
  * weight row per 128-wide K block (moe_grouped_gemm_w4; masked layout only). */
 typedef enum { MOE_WEIGHTS_FP8 = 0, MOE_WEIGHTS_W4 = 1 } moe_weights_t;
+typedef enum { MOE_TYPE_BF16 = 0, MOE_TYPE_FP32 = 1 } moe_type_t;   /* moe_orthogonalise's input */
 
 /* Limits checked by every entry point. */
 #define MOE_MAX_EXPERTS 512
 #define MOE_MAX_TOPK 32
 #define MOE_TILE_M 128
+#define MOE_MAX_SEQUENCES 65535
 
 typedef struct {
     int T;              /* tokens (0 allowed: nothing is launched and the per-token buffers may be
@@ -326,6 +331,127 @@ moe_status_t moe_backward(const moe_config_t* cfg, const void* x, const float* W
                           const int32_t* topk_idx, const float* topk_w, const int32_t* slot_row, const void* fwd_ws,
                           int fwd_train, const void* dy, void* dx, float* dWg, float* db, void* dW13, void* dW2,
                           void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The logits of a training forward. moe_forward_train keeps the router's
+ * logits x W_g^T + b, fp32 [T, E], in its workspace, this many bytes behind its
+ * start; they stay there until the workspace is used again. 0 on a
+ * configuration moe_forward_train does not take.
+ */
+size_t moe_train_logits_offset(const moe_config_t* cfg);
+
+/*
+ * Balance loss and z-loss on the router's logits. Sources: MegaMoE page,
+ * section 2.2, and DeepSeek-V4 lecture page, section 2.3 (an auxiliary loss
+ * that keeps the experts' loads even), DeepSeek MoE page, ch. 1; here in the
+ * product form, load fraction times mean score. p_t = softmax of row t of the
+ * logits. Tokens [seq_offsets[s], seq_offsets[s + 1]) are sequence s; a token
+ * whose mask is 0 is padding and counts nowhere. With n_s = valid tokens of
+ * sequence s, S' = sequences with n_s > 0 and N = sum n_s:
+ *   counts[s, e]    = slots of the sequence's valid tokens with topk_idx = e
+ *   mean_prob[s, e] = 1 / n_s * sum of p_t[e] (0 where n_s = 0)
+ *   loss[0] = alpha / S' * sum_s sum_e E counts[s, e] / (k n_s) * mean_prob[s, e]
+ *   loss[1] = beta / N * sum_t lse_t^2,  lse_t = log sum_e exp(logits[t, e])
+ * (0 where S' = 0). The uniform router has loss[0] = alpha.
+ *   logits      [T, E] fp32 (moe_forward_train's, or moe_route's: its ws)
+ *   topk_idx    [T, k] int32; entries outside [0, E) count nowhere
+ *   token_mask  [T] u8, nullable (every token is valid)
+ *   seq_offsets [S + 1] int32 on the device, non-decreasing, within [0, T];
+ *               nullable with S = 1: one sequence of all T tokens
+ *   loss        [2] fp32 out
+ *   counts      [S, E] int32 out, mean_prob [S, E] fp32 out
+ *   lse         [T] fp32 out: 0 for masked tokens
+ *   seq_valid   [S + 2] int32 out: n_0 .. n_{S-1}, S', N
+ *   ws          scratch of moe_balance_workspace_size(T, E, S) bytes
+ * Sums are fp32 within 296 runs of tokens and fp64 across them, in a fixed
+ * order: results repeat bit for bit. A logit of -inf has p = 0; a valid row
+ * with no finite logit, a NaN or +inf makes its sequence's losses NaN, as the
+ * formula does; masked rows are not read into any result. Tokens outside
+ * [seq_offsets[0], seq_offsets[S]) belong to no sequence: their lse (and their
+ * rows of dlogits below) are left as they were. Offsets that break the rules
+ * are forced into [0, T] and reported (MOE_ERR_CAPACITY in the device status);
+ * the results are then unspecified.
+ * E up to MOE_MAX_EXPERTS, k up to MOE_MAX_TOPK, S up to MOE_MAX_SEQUENCES,
+ * T k below 2^31 (MOE_ERR_UNSUPPORTED_SHAPE above). alpha and beta finite.
+ */
+size_t moe_balance_workspace_size(int T, int E, int S);
+moe_status_t moe_balance_loss(int T, int E, int k, const float* logits, const int32_t* topk_idx,
+                              const uint8_t* token_mask, const int32_t* seq_offsets, int S, float alpha, float beta,
+                              float* loss, int32_t* counts, float* mean_prob, float* lse, int32_t* seq_valid, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* Its gradient with respect to the logits, from the same inputs and the
+ * forward's lse, counts and seq_valid. counts are constants of the gradient:
+ *   dlogits[t, e] = p_t[e] (c[s, e] - sum_j p_t[j] c[s, j])
+ *                   + dloss[1] 2 beta / N lse_t p_t[e],
+ *   c[s, e] = dloss[0] alpha E counts[s, e] / (k n_s^2 S')
+ *   dloss   [2] fp32 on the device, nullable (1, 1)
+ *   dlogits [T, E] fp32 out: 0 for masked tokens */
+moe_status_t moe_balance_loss_backward(int T, int E, int k, const float* logits, const float* lse,
+                                       const int32_t* counts, const int32_t* seq_valid, const uint8_t* token_mask,
+                                       const int32_t* seq_offsets, int S, float alpha, float beta, const float* dloss,
+                                       float* dlogits, void* stream);
+
+/*
+ * A gradient of the logits through the router's linear layer, logits = x W_g^T
+ * + b. moe_backward carries the gradient of the k selected weights; this call
+ * carries one of every logit, as the balance loss has:
+ *   dx  [T, H] bf16 = dx0  + dlogits W_g   (one rounding, to nearest even)
+ *   dWg [E, H] fp32 = dWg0 + dlogits^T x
+ *   db  [E]    fp32 = db0  + column sums of dlogits
+ *   x [T, H] bf16, Wg [E, H] fp32, dlogits [T, E] fp32
+ *   dx0, dWg0, db0  nullable (0): gradients to add to, moe_backward's; each may
+ *                   be its output
+ *   ws  scratch of moe_router_backward_workspace_size(T, H, E) bytes, 256-byte
+ *       aligned
+ * The products run on the tensor cores: dWg with dlogits in three bf16 parts
+ * (its 24 bits) against x, sums promoted to fp32 registers every 128 tokens;
+ * dx with W_g and dlogits in fp16 (11 bits, an eighth of dx's own rounding
+ * step), each expert and then each token scaled by a power of two. Results
+ * repeat bit for bit. A dlogits row of zeros leaves its dx row at dx0. Values
+ * that are not finite spread only as the formulas spread them, except that an
+ * expert whose W_g row holds one makes every dx row NaN or infinite. T = 0 gives the
+ * bases, or zeros.
+ * H as everywhere (a multiple of 128, at most 16384), E up to MOE_MAX_EXPERTS,
+ * T below 2^24.
+ */
+size_t moe_router_backward_workspace_size(int T, int H, int E);
+moe_status_t moe_router_backward(int T, int H, int E, const void* x, const float* Wg, const float* dlogits,
+                                 const void* dx0, const float* dWg0, const float* db0, void* dx, float* dWg, float* db,
+                                 void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Orthogonalised updates of weight matrices (no counterpart on the pages; the
+ * step an optimiser takes with moe_backward's dW13 and dW2 or with momenta of
+ * them): each M x N matrix of G on its own,
+ *   X = G / (|G|_F + eps);  `steps` times: A = X X^T, X <- a X + (b A + c A^2) X
+ *   O = scale X,  bf16, one rounding
+ * (Newton-Schulz steps of the matrix sign in their quintic form; where M > N
+ * the same on X^T). With (a, b, c) = (3.4445, -4.7750, 2.0315) and 5 steps the
+ * singular values of O / scale end between about 0.7 and 1.2.
+ *   batch       entries of G and O; each one matrix [M, N] or, with
+ *               interleaved = 1, two: [2M, N] whose 128-row blocks alternate
+ *               between them (dW13's W1 and W3); M is then a multiple of 128
+ *   G           bf16 (g_type = MOE_TYPE_BF16) or fp32 (MOE_TYPE_FP32)
+ *   O           bf16, G's shape; may not overlap G
+ *   steps       1 .. 32
+ *   ws          scratch of moe_orthogonalise_workspace_size(batch, M, N,
+ *               interleaved) bytes, 256-byte aligned; a large batch is run in
+ *               waves that use it in turn
+ * Products are fp16 with fp32 sums; X is carried in 22 bits, so that the
+ * result differs from exact arithmetic by about bf16's own rounding also where
+ * G is of low rank. A matrix of zeros (with eps > 0) gives zeros; a matrix
+ * with an infinity or a NaN gives NaN, the others of the batch are unaffected.
+ * The coefficients must keep the singular values below 8 and |b x^2 + c x^4|
+ * below 256 from any start in [0, 1] (MOE_ERR_INVALID_ARG otherwise: X would
+ * leave fp16). M, N and batch from 1 (batch 0: nothing is done) to 16384
+ * (MOE_ERR_UNSUPPORTED_SHAPE above). Results repeat bit for bit. The kernel is
+ * a cooperative launch of one block per SM.
+ */
+size_t moe_orthogonalise_workspace_size(int batch, int M, int N, int interleaved);
+moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const void* G, int g_type, int steps, float a,
+                               float b, float c, float eps, float scale, void* O, void* ws, size_t ws_bytes,
+                               void* stream);
 
 /*
  * Auxiliary-loss-free load balancing. Source: MegaMoE page, section 2.2: each

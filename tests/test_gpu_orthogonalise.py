@@ -1,0 +1,152 @@
+"""moe_orthogonalise on the GPU against the 64-bit iteration and against the same iteration with the kernel's roundings.
+
+Tolerances (2-norm of the difference over the 2-norm). Against the exact iteration: rounding to bf16, 2^-8 at most, and
+the roundings of the iteration, at most 2^-7 (asserted on the CPU of the model, for these sizes and kinds).
+Against the model with the same roundings only one step can be compared: kernel and model part where an fp32 sum lands
+on the other side of an fp16 rounding. Sums agree to about 2^-22, so a share 2^-11 of the values of A and B differ by a
+step of 2^-11, in norm 2^-16.5; that makes a share of 2^-8 of the bf16 roundings differ by 2^-8: 2^-12, below 2^-9 with
+room. A second step starts 2^-16.5 apart: a share 2^-5.5 of its fp16 values differ, 2^-14 in norm; the third 2^-12.5;
+from there on the two round independently, and each is only known to be near the exact iterate."""
+import numpy as np
+import pytest
+import torch
+
+from fp8_grouped_gemm_fp32_b200 import api
+from gpu_helpers import ensure_lib
+from test_training_ops_cpu import ortho_matrix
+import training_refs as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def run(G, batch, M, N, inter=False, steps=5, coef=ref.ORTHO, eps=1e-7, scale=1.0, stream=None, ws=None, O=None):
+    ensure_lib()
+    if ws is None:
+        ws = torch.full((api.moe_orthogonalise_workspace_size(batch, M, N, inter),), 0x5a, dtype=torch.uint8, device="cuda")
+    O = torch.full(G.shape, 7.0, dtype=torch.bfloat16, device="cuda") if O is None else O
+    api.moe_orthogonalise(batch, M, N, inter, G, steps, *coef, eps, scale, O, ws, stream)
+    return O
+
+
+def done(O):
+    torch.cuda.synchronize()
+    assert api.moe_get_device_status() == api.MOE_OK
+    return O
+
+
+def close(O, G, steps=5, coef=ref.ORTHO, eps=1e-7, scale=1.0):
+    exact = scale * ref.orthogonalise(G.cpu(), steps, coef, eps)
+    assert ref.rel_norm(O.cpu(), exact) <= 2.0 ** -8 + 2.0 ** -7
+
+
+@pytest.mark.parametrize("M,N", [(1, 1), (1, 300), (300, 1), (5, 7), (64, 64), (100, 260), (260, 100), (257, 513), (384, 128),
+                                 (512, 512), (130, 1000)])
+@pytest.mark.parametrize("kind", ["noise", "low_rank", "decay"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_matches_the_iteration(M, N, kind, dtype):
+    G = torch.stack([(10.0 ** (i - 4)) * ortho_matrix(M, N, kind, i) for i in range(3)]).to(dtype).cuda()
+    O = done(run(G, 3, M, N))
+    for i in range(3):
+        close(O[i], G[i])
+
+
+@pytest.mark.parametrize("M,N", [(1, 1), (1, 300), (300, 1), (5, 7), (64, 64), (100, 260), (260, 100), (257, 513), (384, 128)])
+@pytest.mark.parametrize("kind", ["noise", "low_rank", "decay"])
+def test_one_step_matches_the_model_with_the_same_roundings(M, N, kind):
+    G = ortho_matrix(M, N, kind, 4).to(torch.bfloat16).cuda()[None].contiguous()
+    O = done(run(G, 1, M, N, steps=1))
+    assert ref.rel_norm(O[0].cpu(), ref.orthogonalise_model(G[0].cpu(), 1).to(torch.bfloat16)) <= 2.0 ** -9
+
+
+@pytest.mark.parametrize("M,N", [(128, 64), (256, 512), (384, 130), (640, 600)])
+def test_interleaved_pairs(M, N):
+    pairs = torch.stack([torch.stack([ortho_matrix(M, N, "decay", 2 * i + j) for j in range(2)]) for i in range(3)])
+    G = torch.stack([ref.interleave(q) for q in pairs]).to(torch.bfloat16).cuda()
+    O = done(run(G, 3, M, N, True, scale=0.5))
+    plain = done(run(pairs.reshape(6, M, N).to(torch.bfloat16).cuda(), 6, M, N, scale=0.5))
+    for i in range(3):
+        assert torch.equal(ref.split(O[i]), plain[2 * i:2 * i + 2])       # the layout changes nothing else
+        for j in range(2):
+            close(ref.split(O[i])[j], pairs[i, j].to(torch.bfloat16), scale=0.5)
+
+
+def test_a_batch_of_more_than_one_wave():
+    # waves of a large batch use the workspace in turn: every matrix as if alone
+    M, N, batch = 520, 520, 30
+    G = torch.stack([ortho_matrix(M, N, "decay", i) for i in range(batch)]).to(torch.bfloat16).cuda()
+    assert api.moe_orthogonalise_workspace_size(batch, M, N) < batch * 10 * M * N
+    O = done(run(G, batch, M, N))
+    for i in (0, 13, 24, 25, 29):
+        assert torch.equal(O[i], done(run(G[i:i + 1].contiguous(), 1, M, N))[0])
+
+
+@pytest.mark.parametrize("steps,coef", [(1, ref.ORTHO), (2, (1.5, -0.5, 0.0)), (10, (1.875, -1.25, 0.375)), (32, (1.5, -0.5, 0.0))])
+def test_other_steps_and_coefficients(steps, coef):
+    G = ortho_matrix(200, 310, "noise", 5).cuda()[None].contiguous()
+    close(done(run(G, 1, 200, 310, steps=steps, coef=coef))[0], G[0], steps, coef)
+
+
+def test_zero_matrices_tiny_and_huge_ones():
+    G = torch.stack([ortho_matrix(70, 90, "noise", i) for i in range(5)])
+    G[1] = 0.0
+    G[2] *= 1e-36                                         # its squares are far below fp32
+    G[3] *= 1e36                                          # and above it
+    G = G.cuda()
+    O = done(run(G, 5, 70, 90, eps=1e-30))
+    assert not O[1].any()
+    for i in (0, 2, 3, 4):
+        close(O[i], G[i], eps=1e-30)
+    # where eps is larger than the norm, it damps
+    O = done(run(G, 5, 70, 90, eps=1.0))
+    close(O[0], G[0], eps=1.0)
+    assert not done(run(torch.zeros(1, 70, 90, device="cuda"), 1, 70, 90)).any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_matrix_leaves_the_others_alone(bad):
+    G = torch.stack([ortho_matrix(150, 80, "noise", i) for i in range(3)]).cuda()
+    clean = done(run(G, 3, 150, 80))
+    G[1, 149, 79] = bad
+    O = done(run(G, 3, 150, 80))
+    assert torch.isnan(O[1]).all() and torch.equal(O[0], clean[0]) and torch.equal(O[2], clean[2])
+
+
+def test_rows_beyond_the_matrices_are_left_alone():
+    M, N = 77, 91
+    G = ortho_matrix(M, N, "noise", 3).cuda()[None].contiguous()
+    buf = torch.full((M * N + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    run(G, 1, M, N, O=buf[:M * N].view(1, M, N))
+    done(buf)
+    assert (buf[M * N:] == 7).all()
+
+
+def test_repeats_on_another_stream_and_two_at_once():
+    G = torch.stack([ortho_matrix(300, 520, "decay", i) for i in range(4)]).cuda()
+    want = done(run(G, 4, 300, 520))
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    outs = []
+    for _ in range(3):                                    # two calls in flight, each with its own workspace
+        with torch.cuda.stream(a):
+            outs.append(run(G, 4, 300, 520))
+        with torch.cuda.stream(b):
+            outs.append(run(G, 4, 300, 520))
+    done(want)
+    assert all(torch.equal(o, want) for o in outs)
+
+
+def test_captured_and_replayed_on_new_inputs():
+    G = torch.stack([ortho_matrix(200, 140, "decay", i) for i in range(2)]).cuda()
+    ws = torch.empty(api.moe_orthogonalise_workspace_size(2, 200, 140), dtype=torch.uint8, device="cuda")
+    O = run(G, 2, 200, 140, ws=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+        run(G, 2, 200, 140, ws=ws, O=O)
+    for k in range(2):
+        G.copy_(torch.stack([ortho_matrix(200, 140, "noise", 10 * k + i) for i in range(2)]))
+        torch.cuda.synchronize()
+        g.replay()
+        done(O)
+        for i in range(2):
+            close(O[i], G[i])
