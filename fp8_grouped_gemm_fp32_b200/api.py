@@ -122,18 +122,22 @@ def _p(t: Optional[torch.Tensor]):
     if t is None:
         return None
     if not isinstance(t, torch.Tensor):
-        return ctypes.c_void_p(int(t))
-    if t.numel() and not t.is_cuda:
+        return int(t)
+    ptr = t.data_ptr()                           # 0 for a tensor without elements
+    if ptr and not t.is_cuda:
         raise ValueError("moe_fp8 entry points take CUDA tensors")
     if not t.is_contiguous():
         raise ValueError("moe_fp8 entry points take contiguous tensors")
-    return ctypes.c_void_p(t.data_ptr()) if t.numel() else None
+    return ptr or None
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream):
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        # the current stream's handle, without the Stream object torch.cuda.current_stream() would build
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _check(st: int, call: str):
@@ -227,7 +231,7 @@ def moe_set_contig_kernel(form: int):
 
 # ---------------------------------------------------------------- expert parallelism (see ep.py)
 def _nbytes(t):
-    return t.numel() * t.element_size() if t is not None else 0
+    return t.nbytes if t is not None else 0
 
 
 def moe_ep_workspace_size(cfg: Config) -> int:
@@ -273,6 +277,24 @@ def moe_backward(cfg, x, Wg, W13, S13, W13T, S13T, W2T, S2T, topk_idx, topk_w, s
 
 
 # ---------------------------------------------------------------- balance loss, the router's gradient, updates
+def _args(*tensors):
+    """The tensors' pointers (None and empty ones: null), all checked to be contiguous and on the current device,
+    where the library launches whatever device a pointer is of."""
+    out, dev = [], torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    for t in tensors:
+        ptr = None
+        if t is not None:
+            ptr = t.data_ptr() or None
+            if ptr and not t.is_cuda:
+                raise ValueError("moe_fp8 entry points take CUDA tensors")
+            if ptr and t.get_device() != dev:
+                raise ValueError(f"a tensor of cuda:{t.get_device()} in a call on the current device cuda:{dev}")
+            if not t.is_contiguous():
+                raise ValueError("moe_fp8 entry points take contiguous tensors")
+        out.append(ptr)
+    return out
+
+
 def moe_train_logits(cfg: Config, ws: torch.Tensor) -> torch.Tensor:
     """The router's logits [T, E] fp32 that moe_forward_train left in its workspace (a view of it)."""
     off = int(lib().moe_train_logits_offset(ctypes.byref(cfg)))
@@ -288,17 +310,17 @@ def moe_balance_workspace_size(T: int, E: int, S: int = 1) -> int:
 def moe_balance_loss(T, E, k, logits, topk_idx, token_mask, seq_offsets, S, alpha, beta, loss, counts, mean_prob, lse,
                      seq_valid, ws, stream=None):
     """Balance loss and z-loss of the router's logits; token_mask, seq_offsets nullable."""
-    _check(lib().moe_balance_loss(T, E, k, _p(logits), _p(topk_idx), _p(token_mask), _p(seq_offsets), S, float(alpha),
-                                  float(beta), _p(loss), _p(counts), _p(mean_prob), _p(lse), _p(seq_valid), _p(ws),
-                                  _nbytes(ws), _stream(stream)), "moe_balance_loss")
+    p = _args(logits, topk_idx, token_mask, seq_offsets, loss, counts, mean_prob, lse, seq_valid, ws)
+    _check(lib().moe_balance_loss(T, E, k, *p[:4], S, alpha, beta, *p[4:], _nbytes(ws), _stream(stream)),
+           "moe_balance_loss")
 
 
 def moe_balance_loss_backward(T, E, k, logits, lse, counts, seq_valid, token_mask, seq_offsets, S, alpha, beta, dloss,
                               dlogits, stream=None):
     """dlogits [T, E] of moe_balance_loss; dloss [2] nullable (ones)."""
-    _check(lib().moe_balance_loss_backward(T, E, k, _p(logits), _p(lse), _p(counts), _p(seq_valid), _p(token_mask),
-                                           _p(seq_offsets), S, float(alpha), float(beta), _p(dloss), _p(dlogits),
-                                           _stream(stream)), "moe_balance_loss_backward")
+    p = _args(logits, lse, counts, seq_valid, token_mask, seq_offsets, dloss, dlogits)
+    _check(lib().moe_balance_loss_backward(T, E, k, *p[:6], S, alpha, beta, *p[6:], _stream(stream)),
+           "moe_balance_loss_backward")
 
 
 def moe_router_backward_workspace_size(T: int, H: int, E: int) -> int:
@@ -307,8 +329,8 @@ def moe_router_backward_workspace_size(T: int, H: int, E: int) -> int:
 
 def moe_router_backward(T, H, E, x, Wg, dlogits, dx0, dWg0, db0, dx, dWg, db, ws, stream=None):
     """dx = dx0 + dlogits Wg, dWg = dWg0 + dlogits^T x, db = db0 + sum of dlogits; the bases nullable."""
-    _check(lib().moe_router_backward(T, H, E, _p(x), _p(Wg), _p(dlogits), _p(dx0), _p(dWg0), _p(db0), _p(dx), _p(dWg),
-                                     _p(db), _p(ws), _nbytes(ws), _stream(stream)), "moe_router_backward")
+    p = _args(x, Wg, dlogits, dx0, dWg0, db0, dx, dWg, db, ws)
+    _check(lib().moe_router_backward(T, H, E, *p, _nbytes(ws), _stream(stream)), "moe_router_backward")
 
 
 def moe_orthogonalise_workspace_size(batch: int, M: int, N: int, interleaved: bool = False) -> int:
@@ -319,7 +341,7 @@ def moe_orthogonalise(batch, M, N, interleaved, G, steps, a, b, c, eps, scale, O
     """O = scale * the quintic Newton-Schulz iterate of each matrix of G (bf16 or fp32) after `steps` steps."""
     if G.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("moe_orthogonalise takes bf16 or fp32 matrices")
-    _check(lib().moe_orthogonalise(batch, M, N, int(bool(interleaved)), _p(G),
-                                   TYPE_FP32 if G.dtype == torch.float32 else TYPE_BF16, steps, float(a), float(b),
-                                   float(c), float(eps), float(scale), _p(O), _p(ws), _nbytes(ws), _stream(stream)),
-           "moe_orthogonalise")
+    g, o, w = _args(G, O, ws)
+    _check(lib().moe_orthogonalise(batch, M, N, int(bool(interleaved)), g,
+                                   TYPE_FP32 if G.dtype == torch.float32 else TYPE_BF16, steps, a, b, c, eps, scale, o, w,
+                                   _nbytes(ws), _stream(stream)), "moe_orthogonalise")

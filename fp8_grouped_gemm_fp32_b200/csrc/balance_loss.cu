@@ -10,9 +10,11 @@
 //   dl_t[e] = p_t[e] (c[s, e] - sum_j p_t[j] c[s, j]) + 2 g1 beta / N lse_t p_t[e].
 //
 // Both passes read each logit once, and that read bounds them when T E is large; at a step's usual size the
-// 8 MB of logits sit in L2 and launches are the time, so the forward is two launches (the second resident
-// before the first ends) and the backward one. A group of 8 or 32 lanes takes a token: the row stays in
-// registers between its maximum, its sum and its use. The forward cuts the tokens into at most 296 chunks
+// 8 MB of logits sit in L2 and launches are the time, so the forward is two launches and the backward one, each
+// set up while the one before it runs. A group of 8 or 32 lanes takes a token: the row stays in registers
+// between its maximum, its sum and its use. 32 warps an SM with one row or two each keep enough reads in
+// flight; a row costs about five instructions a value (maximum, exp2 of one fused multiply-add, sum,
+// accumulation), below the memory's pace. The forward cuts the tokens into at most 296 chunks
 // (two blocks an SM); chunk c of sequence s leaves one row of partial sums at index c + s, which is unique
 // because the cuts between chunks and sequences, taken in order, each move c or s up by one. No float is
 // added atomically, so results repeat bit for bit.
@@ -29,16 +31,19 @@ moe_status_t current_device(int* num_sms, int** status);
 
 namespace {
 
-constexpr int kBlThreads = 256;
-constexpr int kBlWarps = kBlThreads / 32;
-constexpr int kMaxChunks = 296;          // two 256-thread blocks on each of 148 SMs
-constexpr int kBwdTokens = 32;           // tokens a backward block takes at least
+constexpr int kFwdThreads = 512, kBwdThreads = 256;
+constexpr int kMaxChunks = 296;          // two forward blocks on each of 148 SMs
+constexpr int kBwdTokens = 16;           // tokens a backward block takes at least
+constexpr float kLog2e = 1.4426950408889634f;
 
-// Tokens of a forward chunk: a multiple of 8, at most kMaxChunks chunks.
-int chunk_tokens(int T) { return std::max(8, ((T + kMaxChunks - 1) / kMaxChunks + 7) / 8 * 8); }
+// Tokens of a forward chunk: a multiple of 16, at most kMaxChunks chunks.
+int chunk_tokens(int T) { return std::max(16, ((T + kMaxChunks - 1) / kMaxChunks + 15) / 16 * 16); }
 int chunks_of(int T) { return (T + chunk_tokens(T) - 1) / chunk_tokens(T); }
 
-constexpr int kRedCols = 32, kRedRows = 16;   // the reducing blocks: columns x partial rows in flight
+// The reduction's blocks: with few sequences, each of up to 296 cuts, 8 columns x 32 rows; with many, whose cuts
+// are few, 32 columns.
+constexpr int kRedThreads = 256, kRedDepth = 10;
+int red_cols(int S) { return S <= 16 ? 8 : 32; }
 
 // The forward's scratch: one row per (chunk, sequence) cut, and each reducing block's share of the loss.
 struct BalWs {
@@ -54,7 +59,7 @@ struct BalWs {
 
 BalWs carve_balance(int T, int E, int S, void* base) {
     BalWs w;
-    const size_t cuts = static_cast<size_t>(chunks_of(T)) + S, nx = (E + kRedCols - 1) / kRedCols;
+    const size_t cuts = static_cast<size_t>(chunks_of(T)) + S, nx = (E + red_cols(S) - 1) / red_cols(S);
     uint8_t* p = static_cast<uint8_t*>(base);
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -78,8 +83,19 @@ __device__ __forceinline__ int seq_start(const int32_t* offsets, int s, int T) {
     return offsets ? min(max(offsets[s], 0), T) : (s ? T : 0);
 }
 
-// The first sequence that ends behind token t (S if none does).
+// The first sequence that ends behind token t (S if none does), the whole block together: the sequences that end
+// before it are counted side by side (one round trip to memory, where a search would take one a step), or, of
+// very many, searched for.
 __device__ __forceinline__ int seq_behind(const int32_t* offsets, int S, int T, int t) {
+    if (!offsets) return 0;
+    if (S <= 4 * static_cast<int>(blockDim.x)) {
+        int n = 0;
+        for (int s0 = 0; s0 < S; s0 += blockDim.x) {
+            const int s = s0 + threadIdx.x;
+            n += __syncthreads_count(s < S && seq_start(offsets, s + 1, T) <= t);
+        }
+        return n;
+    }
     int lo = 0, hi = S;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
@@ -125,37 +141,33 @@ __device__ __forceinline__ float group_sum(float v) {
     return v;
 }
 
-__device__ __forceinline__ void dependents_may_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void wait_for_producer() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// exp(v - m) as 2^(v log2 e - m log2 e); c = m log2 e. Rounding c scales a whole row alike, which its sum undoes.
+__device__ __forceinline__ float exp_from(float v, float c) { return exp2f(fmaf(v, kLog2e, -c)); }
 
 // ---------------------------------------------------------------- forward, pass 1: partial sums of every cut
 // U tokens of each group are in flight together.
 template <int G, int V, bool VEC, int U>
-__global__ void __launch_bounds__(kBlThreads)
+__global__ void __launch_bounds__(kFwdThreads, 2)
 balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                        const uint8_t* __restrict__ mask, const int32_t* __restrict__ offsets, int T, int E, int k,
                        int S, int C, BalWs w, float* __restrict__ lse) {
-    constexpr int kGroups = 32 / G, kRows = kBlWarps * kGroups;     // tokens the block takes at a time
+    constexpr int kGroups = 32 / G, kRows = kFwdThreads / 32 * kGroups;     // tokens the block takes at a time
     extern __shared__ float sm_red[];                               // [kRows][E]
     __shared__ int sm_hist[kMaxE];
     __shared__ float sm_z[kRows];
     __shared__ int sm_n[kRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % G;
     const int row = warp * kGroups + lane / G;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0;
     dependents_may_launch();
+    wait_for_producers();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0;
     const int c0 = blockIdx.x * C, c1 = min(c0 + C, T);
     for (int s = seq_behind(offsets, S, T, c0); s < S; ++s) {
         const int a = max(seq_start(offsets, s, T), c0), b = min(seq_start(offsets, s + 1, T), c1);
         if (a >= c1) break;                          // this sequence, and with it every later one, starts behind
         if (a >= b) continue;
-        for (int e = threadIdx.x; e < E; e += kBlThreads) sm_hist[e] = 0;
+        for (int e = threadIdx.x; e < E; e += kFwdThreads) sm_hist[e] = 0;
         __syncthreads();
-        for (int i = threadIdx.x; i < (b - a) * k; i += kBlThreads) {
-            const int t = a + i / k;
-            const int e = idx[static_cast<int64_t>(a) * k + i];
-            if ((!mask || mask[t]) && e >= 0 && e < E) atomicAdd(&sm_hist[e], 1);
-        }
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -169,6 +181,11 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
                 const int t = t0 + u * kRows + row;
                 on[u] = t < b && (!mask || mask[t]);
                 load_row<G, V, VEC>(logits + static_cast<int64_t>(on[u] ? t : a) * E, E, j, -INFINITY, v[u]);
+                if (on[u])
+                    for (int i = j; i < k; i += G) {
+                        const int e = idx[static_cast<int64_t>(t) * k + i];
+                        if (e >= 0 && e < E) atomicAdd(&sm_hist[e], 1);
+                    }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -176,11 +193,12 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
 #pragma unroll
                 for (int i = 1; i < V; ++i) m = fmaxf(m, v[u][i]);   // a NaN comes back through the sum
                 m = group_max<G>(m);
+                const float mc = m * kLog2e;
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    // a lane's places behind the last expert hold -inf and give exp = 0, unless m is -inf too
-                    v[u][i] = expert_of<G, VEC>(i, j) < E ? expf(v[u][i] - m) : 0.0f;
+                    // a lane's places behind the last expert hold -inf: 0, or NaN in a row that is NaN anyway
+                    v[u][i] = exp_from(v[u][i], mc);
                     sum += v[u][i];
                 }
                 sum = group_sum<G>(sum);
@@ -205,7 +223,7 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
         if (j == 0) { sm_z[row] = z; sm_n[row] = n; }
         __syncthreads();
         const int64_t cut = static_cast<int64_t>(blockIdx.x) + s;
-        for (int e = threadIdx.x; e < E; e += kBlThreads) {
+        for (int e = threadIdx.x; e < E; e += kFwdThreads) {
             float x = 0.0f;
 #pragma unroll 8
             for (int r = 0; r < kRows; ++r) x += sm_red[r * E + e];
@@ -223,34 +241,31 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
     }
 }
 
-template <typename X>
-__device__ __forceinline__ X block_sum(X v, X* scratch) {
-    constexpr int kW = kRedCols * kRedRows / 32;
+__device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    X s = 0;
-#pragma unroll
-    for (int i = 0; i < kW; ++i) s += scratch[i];
-    return s;
+    return v;
 }
 
 // ---------------------------------------------------------------- forward, pass 2: the cuts of each sequence
-// Grid (column blocks, sequences). The last block to finish adds the blocks' shares of the losses in a fixed order.
-__global__ void __launch_bounds__(kRedCols * kRedRows)
+// Grid (column blocks, sequences); COLS columns a block, 256 / COLS partial rows side by side and kRedDepth of
+// those in flight. The last block to finish adds the blocks' shares of the losses in a fixed order.
+template <int COLS>
+__global__ void __launch_bounds__(kRedThreads)
 balance_reduce_kernel(const int32_t* __restrict__ offsets, int T, int E, int k, int S, int C, float alpha, float beta,
                       BalWs w, float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ mean_prob,
                       int32_t* valid, int* status) {
-    __shared__ float sm_p[kRedRows][kRedCols + 1];
-    __shared__ int sm_h[kRedRows][kRedCols + 1];
-    __shared__ double sm_d[kRedCols * kRedRows / 32];
-    __shared__ int sm_i[kRedCols * kRedRows / 32];
+    constexpr int kRows = kRedThreads / COLS, kW = kRedThreads / 32;
+    __shared__ float sm_p[kW][COLS];
+    __shared__ int sm_h[kW][COLS];
+    __shared__ double sm_z[kW], sm_z2[kW];
+    __shared__ int sm_n[kW], sm_n2[kW];
     __shared__ bool sm_last;
-    const int col = threadIdx.x % kRedCols, r0 = threadIdx.x / kRedCols, s = blockIdx.y;
-    const int e = blockIdx.x * kRedCols + col;
-    wait_for_producer();
+    const int col = threadIdx.x % COLS, r0 = threadIdx.x / COLS, s = blockIdx.y;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e = blockIdx.x * COLS + col;
+    dependents_may_launch();
+    wait_for_producers();
     const int a = seq_start(offsets, s, T), b = seq_start(offsets, s + 1, T);
     if (offsets && threadIdx.x == 0 && blockIdx.x == 0 && (offsets[s] != a || offsets[s + 1] != b || a > b))
         set_status(status, kStatusCapacity);
@@ -258,57 +273,83 @@ balance_reduce_kernel(const int32_t* __restrict__ offsets, int T, int E, int k, 
     float p = 0.0f;
     int h = 0, n = 0;
     double z = 0.0;
+    for (int c = lo + threadIdx.x; c < hi; c += kRedThreads) {
+        n += w.nval[c + s];
+        if (blockIdx.x == 0) z += w.zsum[c + s];
+    }
     if (e < E) {
-#pragma unroll 4
-        for (int c = lo + r0; c < hi; c += kRedRows) {
-            p += w.psum[(static_cast<int64_t>(c) + s) * E + e];
-            h += w.hist[(static_cast<int64_t>(c) + s) * E + e];
+        for (int c0 = lo + r0; c0 < hi; c0 += kRows * kRedDepth) {
+            float pv[kRedDepth];
+            int hv[kRedDepth];
+#pragma unroll
+            for (int i = 0; i < kRedDepth; ++i) {
+                const int64_t at = (static_cast<int64_t>(c0) + i * kRows + s) * E + e;
+                const bool in = c0 + i * kRows < hi;
+                pv[i] = in ? w.psum[at] : 0.0f;
+                hv[i] = in ? w.hist[at] : 0;
+            }
+#pragma unroll
+            for (int i = 0; i < kRedDepth; ++i) { p += pv[i]; h += hv[i]; }
         }
     }
-    for (int c = lo + threadIdx.x; c < hi; c += kRedCols * kRedRows) {
-        n += w.nval[c + s];
-        z += w.zsum[c + s];
-    }
-    sm_p[r0][col] = p;
-    sm_h[r0][col] = h;
-    n = block_sum(n, sm_i);
-    if (blockIdx.x == 0) z = block_sum(z, sm_d);
-    double share = 0.0;
-    if (r0 == 0 && e < E) {
-        double ps = 0.0;
-        int hs = 0;
 #pragma unroll
-        for (int r = 0; r < kRedRows; ++r) { ps += sm_p[r][col]; hs += sm_h[r][col]; }
-        const double mean = n > 0 ? ps / n : 0.0;
-        mean_prob[static_cast<int64_t>(s) * E + e] = static_cast<float>(mean);
-        counts[static_cast<int64_t>(s) * E + e] = hs;
-        share = n > 0 ? mean * hs * E / (static_cast<double>(k) * n) : 0.0;
+    for (int o = COLS; o < 32; o <<= 1) {
+        p += __shfl_xor_sync(0xffffffffu, p, o);
+        h += __shfl_xor_sync(0xffffffffu, h, o);
     }
-    share = block_sum(share, sm_d);
-    if (threadIdx.x == 0) {
-        w.part[static_cast<int64_t>(s) * gridDim.x + blockIdx.x] = share;
-        if (blockIdx.x == 0) { w.zpart[s] = z; valid[s] = n; }
-        __threadfence();
-        sm_last = atomicAdd(w.ticket, 1u) == gridDim.x * gridDim.y - 1;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (blockIdx.x == 0) z = warp_sum(z);
+    if (lane < COLS) { sm_p[warp][lane] = p; sm_h[warp][lane] = h; }
+    if (lane == 0) { sm_n[warp] = n; sm_z[warp] = z; }
+    __syncthreads();
+    if (warp == 0) {
+        n = 0;
+        z = 0.0;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) { n += sm_n[i]; z += sm_z[i]; }
+        double share = 0.0;
+        if (lane < COLS && e < E) {
+            double ps = 0.0;
+            int hs = 0;
+#pragma unroll
+            for (int i = 0; i < kW; ++i) { ps += sm_p[i][lane]; hs += sm_h[i][lane]; }
+            const double inv = n > 0 ? 1.0 / n : 0.0;
+            mean_prob[static_cast<int64_t>(s) * E + e] = static_cast<float>(ps * inv);
+            counts[static_cast<int64_t>(s) * E + e] = hs;
+            share = ps * hs * inv * inv;                     // times E / k at the end
+        }
+        share = warp_sum(share);
+        if (lane == 0) {
+            w.part[static_cast<int64_t>(s) * gridDim.x + blockIdx.x] = share;
+            if (blockIdx.x == 0) { w.zpart[s] = z; valid[s] = n; }
+            __threadfence();
+            sm_last = atomicAdd(w.ticket, 1u) == gridDim.x * gridDim.y - 1;
+        }
     }
     __syncthreads();
     if (!sm_last) return;
     __threadfence();
     double l0 = 0.0, l1 = 0.0;
     int full = 0, total = 0;
-    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(S) * gridDim.x; i += kRedCols * kRedRows) l0 += __ldcg(w.part + i);
-    for (int i = threadIdx.x; i < S; i += kRedCols * kRedRows) {
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(S) * gridDim.x; i += kRedThreads) l0 += __ldcg(w.part + i);
+    for (int i = threadIdx.x; i < S; i += kRedThreads) {
         const int v = __ldcg(valid + i);
         l1 += __ldcg(w.zpart + i);
         full += v > 0;
         total += v;
     }
-    l0 = block_sum(l0, sm_d);
-    l1 = block_sum(l1, sm_d);
-    full = block_sum(full, sm_i);
-    total = block_sum(total, sm_i);
+    l0 = warp_sum(l0);
+    l1 = warp_sum(l1);
+    full = __reduce_add_sync(0xffffffffu, full);
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (lane == 0) { sm_z[warp] = l0; sm_z2[warp] = l1; sm_n[warp] = full; sm_n2[warp] = total; }
+    __syncthreads();
     if (threadIdx.x == 0) {
-        loss[0] = static_cast<float>(alpha * l0 / max(full, 1));
+        l0 = l1 = 0.0;
+        full = total = 0;
+#pragma unroll
+        for (int i = 0; i < kW; ++i) { l0 += sm_z[i]; l1 += sm_z2[i]; full += sm_n[i]; total += sm_n2[i]; }
+        loss[0] = static_cast<float>(alpha * l0 * E / (static_cast<double>(k) * max(full, 1)));
         loss[1] = static_cast<float>(beta * l1 / max(total, 1));
         valid[S] = full;
         valid[S + 1] = total;
@@ -317,16 +358,18 @@ balance_reduce_kernel(const int32_t* __restrict__ offsets, int T, int E, int k, 
 
 // ---------------------------------------------------------------- backward
 template <int G, int V, bool VEC, int U>
-__global__ void __launch_bounds__(kBlThreads)
+__global__ void __launch_bounds__(kBwdThreads, 4)
 balance_backward_kernel(const float* __restrict__ logits, const float* __restrict__ lse,
                         const int32_t* __restrict__ counts, const int32_t* __restrict__ valid,
                         const uint8_t* __restrict__ mask, const int32_t* __restrict__ offsets, int T, int E, int k,
                         int S, int C, float alpha, float beta, const float* __restrict__ dloss,
                         float* __restrict__ dlogits) {
-    constexpr int kGroups = 32 / G, kRows = kBlWarps * kGroups;
+    constexpr int kGroups = 32 / G, kRows = kBwdThreads / 32 * kGroups;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % G;
     const int row = warp * kGroups + lane / G;
     const int c0 = blockIdx.x * C, c1 = min(c0 + C, T);
+    dependents_may_launch();
+    wait_for_producers();
     const float g0 = dloss ? dloss[0] : 1.0f, g1 = dloss ? dloss[1] : 1.0f;
     const float zc = 2.0f * g1 * beta / static_cast<float>(max(valid[S + 1], 1));
     for (int s = seq_behind(offsets, S, T, c0); s < S; ++s) {
@@ -354,10 +397,11 @@ balance_backward_kernel(const float* __restrict__ logits, const float* __restric
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                const float lc = l[u] * kLog2e;
                 float dot = 0.0f;
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    v[u][i] = expert_of<G, VEC>(i, j) < E ? expf(v[u][i] - l[u]) : 0.0f;
+                    v[u][i] = exp_from(v[u][i], lc);
                     dot = fmaf(v[u][i], c[i], dot);
                 }
                 dot = group_sum<G>(dot);
@@ -392,9 +436,9 @@ struct RowForm { static constexpr int G = G_, V = V_, U = U_; static constexpr b
 template <typename F>
 cudaError_t with_row_form(int E, F f) {
     const bool vec = E % 4 == 0;
-    if (E <= 64) return vec ? f(RowForm<8, 8, true, 4>()) : f(RowForm<8, 8, false, 4>());
-    if (E <= 256) return vec ? f(RowForm<32, 8, true, 4>()) : f(RowForm<32, 8, false, 4>());
-    return vec ? f(RowForm<32, 16, true, 2>()) : f(RowForm<32, 16, false, 2>());
+    if (E <= 64) return vec ? f(RowForm<8, 8, true, 2>()) : f(RowForm<8, 8, false, 2>());
+    if (E <= 256) return vec ? f(RowForm<32, 8, true, 2>()) : f(RowForm<32, 8, false, 2>());
+    return vec ? f(RowForm<32, 16, true, 1>()) : f(RowForm<32, 16, false, 1>());
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -440,27 +484,19 @@ moe_status_t moe_balance_loss(int T, int E, int k, const float* logits, const in
     if (T > 0) {
         err = with_row_form(E, [&](auto f) {
             using F = decltype(f);
-            balance_partial_kernel<F::G, F::V, F::VEC, F::U>
-                <<<chunks_of(T), kBlThreads, sizeof(float) * kBlWarps * (32 / F::G) * E, s>>>(
-                    logits, topk_idx, token_mask, seq_offsets, T, E, k, S, C, w, lse);
-            return cudaGetLastError();
+            return launch_dependent(balance_partial_kernel<F::G, F::V, F::VEC, F::U>, dim3(chunks_of(T)), dim3(kFwdThreads),
+                                    sizeof(float) * (kFwdThreads / 32) * (32 / F::G) * E, s, logits, topk_idx, token_mask,
+                                    seq_offsets, T, E, k, S, C, w, lse);
         });
     } else {
         err = cudaMemsetAsync(w.ticket, 0, sizeof(unsigned), s);   // no tokens: the reduction alone, over nothing
     }
-    if (err != cudaSuccess) return MOE_ERR_CUDA;
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((E + kRedCols - 1) / kRedCols, S);
-    cfg.blockDim = dim3(kRedCols * kRedRows);
-    cfg.stream = s;
-    // the reduction may be set up while the partial sums run; it waits for them before it reads
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = T > 0 ? 1 : 0;
-    err = cudaLaunchKernelEx(&cfg, balance_reduce_kernel, seq_offsets, T, E, k, S, C, alpha, beta, w, loss, counts,
-                             mean_prob, seq_valid, status);
+    if (err == cudaSuccess) {
+        const int cols = red_cols(S);
+        err = launch_dependent(cols == 8 ? balance_reduce_kernel<8> : balance_reduce_kernel<32>, dim3((E + cols - 1) / cols, S),
+                               dim3(kRedThreads), 0, s, seq_offsets, T, E, k, S, C, alpha, beta, w, loss, counts, mean_prob,
+                               seq_valid, status);
+    }
     return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -479,12 +515,11 @@ moe_status_t moe_balance_loss_backward(int T, int E, int k, const float* logits,
     const cudaError_t err = with_row_form(E, [&](auto f) {
         using F = decltype(f);
         // a block's tokens: whole turns of its rows, several only where enough blocks are left to fill the GPU
-        const int turn = kBlWarps * (32 / F::G) * F::U;
+        const int turn = kBwdThreads / 32 * (32 / F::G) * F::U;
         const int C = std::max(std::max(kBwdTokens, turn), (T / (4 * num_sms) + turn - 1) / turn * turn);
-        balance_backward_kernel<F::G, F::V, F::VEC, F::U>
-            <<<(T + C - 1) / C, kBlThreads, 0, static_cast<cudaStream_t>(stream)>>>(
-                logits, lse, counts, seq_valid, token_mask, seq_offsets, T, E, k, S, C, alpha, beta, dloss, dlogits);
-        return cudaGetLastError();
+        return launch_dependent(balance_backward_kernel<F::G, F::V, F::VEC, F::U>, dim3((T + C - 1) / C), dim3(kBwdThreads), 0,
+                                static_cast<cudaStream_t>(stream), logits, lse, counts, seq_valid, token_mask, seq_offsets, T,
+                                E, k, S, C, alpha, beta, dloss, dlogits);
     });
     return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
