@@ -4,9 +4,9 @@
 // matrix sign, in the quintic form), and O = scale X.
 //
 // All of it is matrix products, and the tensor cores bound it: with s <= l the sides, a step is s^2 l (A: half
-// of a symmetric product) + s^3 (A^2, half) + 2 s^2 l multiply-adds x 2. One persistent kernel of CTA pairs
-// runs every product of every step (256 x 256 tiles, tcgen05 cta_group::2, K blocks of 64 by TMA in a ring,
-// two accumulators in tensor memory). A tile waits on its own matrix's counter only, so the matrices of a
+// of a symmetric product) + s^3 (A^2, half) + 2 s^2 l flops. One persistent kernel runs every product of every
+// step: 256 x 256 tiles of CTA pairs (tcgen05 cta_group::2), or 128 x 128 tiles of single CTAs where there are
+// few; K blocks of 64 by TMA in a ring, two accumulators in tensor memory. A tile waits on its own matrix's counter only, so the matrices of a
 // batch fill each other's dependencies and the tail of one product overlaps the head of the next; symmetric
 // products compute the tiles on and below the diagonal and store each twice, the second time transposed.
 //
@@ -32,7 +32,6 @@ moe_status_t current_device(int* num_sms, int** status);
 namespace {
 
 constexpr uint64_t kOrthoWaitNs = 4000000000ull;
-constexpr int kOT = 256;                     // tile edge of a CTA pair
 constexpr int kOK = 64;                      // K values a stage holds: 128 bytes
 constexpr int kOStages = 5;
 constexpr int kOBox = 64 * kOK * 2;          // one 64 x 64 box of an operand: 8 KB
@@ -51,6 +50,7 @@ struct SmemO {
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t eload[kOEpi];
+    uint64_t stored;
     uint32_t tmem_base;
     volatile int abort_flag;
 };
@@ -72,7 +72,7 @@ struct OrthoArgs {
     float out_scale;         // scale / the power of two X is stored with
     float gram_scale;        // 64 / that power squared
     uint16_t* O;             // the wave's first matrix
-    unsigned* done;          // [mats] finished warps of tiles
+    unsigned* done;          // [mats] finished tiles, counted by every CTA
     int* status;
 };
 
@@ -81,27 +81,30 @@ struct OrthoTile {
     int step, prod, b, ti, tj;
 };
 
+template <bool PAIR>
 struct OrthoShape {
+    static constexpr int kEdge = PAIR ? 256 : 128;
     int s, l, nb, rb, cb, ns, nu;     // sides, tiles: symmetric per side, update rows / columns, per product
     bool tall;
     __device__ OrthoShape(const OrthoArgs& g) {
         tall = g.M > g.N;
         s = min(g.M, g.N);
         l = max(g.M, g.N);
-        nb = (s + kOT - 1) / kOT;
+        nb = (s + kEdge - 1) / kEdge;
         ns = nb * (nb + 1) / 2;
-        rb = (g.M + kOT - 1) / kOT;
-        cb = (g.N + kOT - 1) / kOT;
+        rb = (g.M + kEdge - 1) / kEdge;
+        cb = (g.N + kEdge - 1) / kEdge;
         nu = rb * cb;
     }
 };
 
 // Walks this cluster's tiles: products in order, each over all matrices, every `stride`-th tile.
+template <bool PAIR>
 struct OrthoWalk {
     const OrthoArgs& g;
-    const OrthoShape& sh;
+    const OrthoShape<PAIR>& sh;
     int pos, step, prod, stride;
-    __device__ OrthoWalk(const OrthoArgs& g_, const OrthoShape& sh_, int first, int stride_)
+    __device__ OrthoWalk(const OrthoArgs& g_, const OrthoShape<PAIR>& sh_, int first, int stride_)
         : g(g_), sh(sh_), pos(first), step(0), prod(0), stride(stride_) {
         settle();
     }
@@ -133,10 +136,11 @@ struct OrthoWalk {
         }
         return t;
     }
-    // Finished warps of tiles its matrix needs before this tile may start: all earlier products'.
+    // Finished tiles (each CTA of a pair counts its half) its matrix needs before this tile may start: all
+    // earlier products'.
     __device__ unsigned needs() const {
         const int tiles = step * (2 * sh.ns + sh.nu) + prod * sh.ns;
-        return static_cast<unsigned>(tiles) * (2 * kOEpi);
+        return static_cast<unsigned>(tiles) * (PAIR ? 2 : 1);
     }
 };
 
@@ -159,14 +163,17 @@ __device__ __forceinline__ int64_t user_row(int m, int r, int M, int interleaved
     return static_cast<int64_t>(m >> 1) * 2 * M + (r / kGroup * 2 + (m & 1)) * kGroup + r % kGroup;
 }
 
+template <bool PAIR>
 __global__ void __launch_bounds__(kOThreads, 1)
 ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant__ OrthoArgs g) {
     extern __shared__ uint8_t smem_raw[];
     SmemO& sm = *reinterpret_cast<SmemO*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const OrthoShape sh(g);
-    OrthoWalk w(g, sh, static_cast<int>(cluster_id_x()), static_cast<int>(cluster_count_x()));
+    constexpr int kEdge = PAIR ? 256 : 128;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+    const OrthoShape<PAIR> sh(g);
+    OrthoWalk<PAIR> w(g, sh, static_cast<int>(PAIR ? cluster_id_x() : blockIdx.x),
+                      static_cast<int>(PAIR ? cluster_count_x() : gridDim.x));
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kOStages; ++s) {
@@ -175,25 +182,26 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.tfull[i], 1);
-            mbar_init(&sm.tempty[i], 2 * kOEpi);
+            mbar_init(&sm.tempty[i], (PAIR ? 2 : 1) * kOEpi);
         }
         for (int i = 0; i < kOEpi; ++i) mbar_init(&sm.eload[i], 1);
+        mbar_init(&sm.stored, kOEpi);
         sm.abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 1) {
-        tmem_alloc_pair(&sm.tmem_base, 512);
-        tmem_relinquish_pair();
+        if constexpr (PAIR) { tmem_alloc_pair(&sm.tmem_base, 512); tmem_relinquish_pair(); }
+        else { tmem_alloc(&sm.tmem_base, 512); tmem_relinquish(); }
     }
     tc_fence_before();
-    cluster_sync();
+    if constexpr (PAIR) cluster_sync(); else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
 
     auto fail = [&]() {
         set_status(g.status, kStatusTimeout);
         sm.abort_flag = 1;
-        st_shared_cluster_u32(mapa_shared(smem_u32((const void*)&sm.abort_flag), rank ^ 1u), 1u);
+        if constexpr (PAIR) st_shared_cluster_u32(mapa_shared(smem_u32((const void*)&sm.abort_flag), rank ^ 1u), 1u);
     };
     // Waits until matrix b's counter reaches `need`, then lets later TMA accesses see what was stored before it.
     auto wait_for = [&](int b, unsigned need) -> bool {
@@ -201,7 +209,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
             const uint64_t t0 = globaltimer_ns();
             while (load_acquire_gpu(g.done + b) < need) {
                 if (sm.abort_flag || globaltimer_ns() - t0 > kOrthoWaitNs) return false;
-                __nanosleep(64);
+                __nanosleep(20);
             }
         }
         fence_proxy_async();
@@ -223,17 +231,22 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                 const bool a_mn = t.prod == 0 && sh.tall;
                 const bool b_mn = (t.prod == 0 && sh.tall) || (t.prod == 2 && !sh.tall);
                 const int K = t.prod == 0 ? sh.l : sh.s;
-                const int ra = t.ti * kOT + static_cast<int>(rank) * 128, rb = t.tj * kOT + static_cast<int>(rank) * 128;
+                const int ra = t.ti * kEdge + static_cast<int>(rank) * 128, rb = t.tj * kEdge + static_cast<int>(rank) * 128;
                 for (int k0 = 0; k0 < K; k0 += kOK, ++it) {
                     const int s = it % kOStages;
                     if (!mbar_wait(&sm.empty[s], ((it / kOStages) & 1) ^ 1, kOrthoWaitNs)) { fail(); ok = false; break; }
-                    const uint32_t fb = mapa_shared(smem_u32(&sm.full[s]), 0);
-                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], 4 * kOOper);
+                    const uint32_t fb = PAIR ? mapa_shared(smem_u32(&sm.full[s]), 0) : 0u;
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], (PAIR ? 4 : 2) * kOOper);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int ya = ra + 64 * i, yb = rb + 64 * i;
-                        tma_load_3d_pair(sm.a[s] + i * kOBox, ma, fb, a_mn ? ya : k0, a_mn ? k0 : ya, t.b);
-                        tma_load_3d_pair(sm.b[s] + i * kOBox, mb, fb, b_mn ? yb : k0, b_mn ? k0 : yb, t.b);
+                        if constexpr (PAIR) {
+                            tma_load_3d_pair(sm.a[s] + i * kOBox, ma, fb, a_mn ? ya : k0, a_mn ? k0 : ya, t.b);
+                            tma_load_3d_pair(sm.b[s] + i * kOBox, mb, fb, b_mn ? yb : k0, b_mn ? k0 : yb, t.b);
+                        } else {
+                            tma_load_3d(sm.a[s] + i * kOBox, ma, &sm.full[s], a_mn ? ya : k0, a_mn ? k0 : ya, t.b);
+                            tma_load_3d(sm.b[s] + i * kOBox, mb, &sm.full[s], b_mn ? yb : k0, b_mn ? k0 : yb, t.b);
+                        }
                     }
                 }
             }
@@ -248,8 +261,8 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                 const bool a_mn = t.prod == 0 && sh.tall;
                 const bool b_mn = (t.prod == 0 && sh.tall) || (t.prod == 2 && !sh.tall);
                 const int K = t.prod == 0 ? sh.l : sh.s;
-                const uint32_t idesc = f16_idesc(2 * 128, kOT, false, a_mn, b_mn);
-                const uint32_t buf = ti & 1, d = tmem + buf * kOT;
+                const uint32_t idesc = f16_idesc(kEdge, kEdge, false, a_mn, b_mn);
+                const uint32_t buf = ti & 1, d = tmem + buf * kEdge;
                 if (!mbar_wait(&sm.tempty[buf], ((ti >> 1) & 1) ^ 1, kOrthoWaitNs)) { fail(); break; }
                 tc_fence_after();
                 for (int k0 = 0; k0 < K; k0 += kOK, ++it) {
@@ -262,32 +275,35 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                         // 16 K values: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major box
                         const uint64_t da = a_mn ? sw128_mnmajor_desc(a0 + kk * 2048, kOBox) : sw128_kmajor_desc(a0 + kk * 32);
                         const uint64_t db = b_mn ? sw128_mnmajor_desc(b0 + kk * 2048, kOBox) : sw128_kmajor_desc(b0 + kk * 32);
-                        umma_f16_pair(d, da, db, idesc, k0 + kk > 0);
+                        if constexpr (PAIR) umma_f16_pair(d, da, db, idesc, k0 + kk > 0);
+                        else umma_f16(d, da, db, idesc, k0 + kk > 0);
                     }
-                    umma_commit_pair(&sm.empty[s], 0x3);
+                    if constexpr (PAIR) umma_commit_pair(&sm.empty[s], 0x3); else umma_commit(&sm.empty[s]);
                 }
-                if (ok) umma_commit_pair(&sm.tfull[buf], 0x3);
+                if (ok) { if constexpr (PAIR) umma_commit_pair(&sm.tfull[buf], 0x3); else umma_commit(&sm.tfull[buf]); }
             }
         }
     } else if (warp >= 4) {
         // ---------------- epilogue: warp = lane quadrant q x column half; 64 columns at a time through its stage
         const int ew = warp - 4, q = warp & 3, half = ew >> 2;
         const uint32_t st0 = smem_u32(sm.stage[ew][0]), st1 = smem_u32(sm.stage[ew][1]);
-        const uint32_t tempty0 = mapa_shared(smem_u32(&sm.tempty[0]), 0);
-        uint32_t ti = 0, loads = 0;
+        const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&sm.tempty[0]), 0) : 0u;
+        constexpr int kSubs = kEdge / 128;
+        const float quad = g.c * (1.0f / kPScale), inv = 1.0f / kPScale;
+        uint32_t ti = 0, loads = 0, tiles = 0;
         bool ok = true;
         for (; ok && w.more(); w.next(), ++ti) {
             if (sm.abort_flag) break;
             const OrthoTile t = w.tile();
             const uint32_t buf = ti & 1;
-            const int row0 = t.ti * kOT + static_cast<int>(rank) * 128 + q * 32;
+            const int row0 = t.ti * kEdge + static_cast<int>(rank) * 128 + q * 32;
             const int rows = t.prod == 2 ? g.M : sh.s, cols = t.prod == 2 ? g.N : sh.s;
             const int cur = t.step & 1;
             const bool last = t.prod == 2 && t.step == g.steps - 1;
             const bool mirror = t.prod != 2 && t.ti != t.tj;
 #pragma unroll 1
-            for (int sub = 0; sub < 2; ++sub) {
-                const int col0 = t.tj * kOT + half * 128 + sub * 64;
+            for (int sub = 0; sub < kSubs; ++sub) {
+                const int col0 = t.tj * kEdge + half * (kEdge / 2) + sub * 64;
                 // the stage is free once the last stores have read it; then the tile's own values come in
                 int good = 1;
                 if (lane == 0) {
@@ -314,79 +330,97 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                     if (!mbar_wait(&sm.eload[ew], loads & 1, kOrthoWaitNs)) { fail(); ok = false; break; }
                     ++loads;
                 }
-                const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kOT + half * 128 + sub * 64;
+                const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * kEdge + half * (kEdge / 2) + sub * 64;
                 float v[2][32];
                 tmem_ld32(taddr, v[0]);
                 tmem_ld32(taddr + 32, v[1]);
                 tmem_ld_wait();
-                if (sub == 1) {
+                if (sub == kSubs - 1) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
-                        if (rank) mbar_arrive_cluster(tempty0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
+                        if (PAIR && rank) mbar_arrive_cluster(tempty0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
                         else mbar_arrive(&sm.tempty[buf]);
                     }
                 }
-                // 16-byte piece p (8 columns) of row `lane` sits at p ^ (lane & 7) (128-byte swizzle)
+                // 16-byte piece p (8 columns) of row `lane` sits at p ^ (lane & 7) (128-byte swizzle); four at a time,
+                // all of a turn's reads before its writes, which are in place
+                auto at = [&](int p) { return static_cast<uint32_t>(lane * 128 + ((p ^ (lane & 7)) << 4)); };
 #pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    const uint32_t at = static_cast<uint32_t>(lane * 128 + ((p ^ (lane & 7)) << 4));
-                    float x[8];
+                for (int hp = 0; hp < 2; ++hp) {
+                    float (&x)[32] = v[hp];
+                    uint32_t o[4][4];
+                    if (t.prod == 2) {
+                        uint4 u[4], r[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = v[p >> 2][(p & 3) * 8 + i];
-                    if (t.prod == 0) {
+                        for (int p = 0; p < 4; ++p) { u[p] = ld_shared_v4(st0 + at(hp * 4 + p)); r[p] = ld_shared_v4(st1 + at(hp * 4 + p)); }
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] *= g.gram_scale;
-                    } else if (t.prod == 1) {
-                        const uint4 u = ld_shared_v4(st0 + at);
-                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 f = unpack_half2(uu[i]);
-                            x[2 * i] = fmaf(g.b, f.x, g.c * (1.0f / kPScale) * x[2 * i]);
-                            x[2 * i + 1] = fmaf(g.b, f.y, g.c * (1.0f / kPScale) * x[2 * i + 1]);
-                        }
-                    } else {
-                        const uint4 u = ld_shared_v4(st0 + at), r = ld_shared_v4(st1 + at);
-                        const uint32_t uu[4] = {u.x, u.y, u.z, u.w}, rr[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 h = unpack_half2(uu[i]), lo = unpack_half2(rr[i]);
-                            x[2 * i] = fmaf(g.a, h.x + lo.x, (1.0f / kPScale) * x[2 * i]);
-                            x[2 * i + 1] = fmaf(g.a, h.y + lo.y, (1.0f / kPScale) * x[2 * i + 1]);
-                        }
-                    }
-                    uint32_t o[4];
-                    if (last) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(g.out_scale * x[2 * i], g.out_scale * x[2 * i + 1]);
-                            o[i] = *reinterpret_cast<const uint32_t*>(&b2);
-                        }
-                        st_shared_v4(st0 + at, o[0], o[1], o[2], o[3]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) o[i] = pack_half2(x[2 * i], x[2 * i + 1]);
-                        st_shared_v4(st0 + at, o[0], o[1], o[2], o[3]);
-                        if (t.prod == 2) {
-                            uint32_t r[4];
+                        for (int p = 0; p < 4; ++p) {
+                            const uint32_t uu[4] = {u[p].x, u[p].y, u[p].z, u[p].w}, rr[4] = {r[p].x, r[p].y, r[p].z, r[p].w};
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
-                                const float2 h = unpack_half2(o[i]);
-                                r[i] = pack_half2(x[2 * i] - h.x, x[2 * i + 1] - h.y);
+                                const float2 h = unpack_half2(uu[i]), lo = unpack_half2(rr[i]);
+                                float& x0 = x[p * 8 + 2 * i];
+                                float& x1 = x[p * 8 + 2 * i + 1];
+                                const float2 y = __ffma2_rn(make_float2(g.a, g.a), __fadd2_rn(h, lo),
+                                                            __fmul2_rn(make_float2(inv, inv), make_float2(x0, x1)));
+                                x0 = y.x;
+                                x1 = y.y;
+                                if (last) {
+                                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(g.out_scale * x0, g.out_scale * x1);
+                                    o[p][i] = *reinterpret_cast<const uint32_t*>(&b2);
+                                } else {
+                                    o[p][i] = pack_half2(x0, x1);
+                                }
                             }
-                            st_shared_v4(st1 + at, r[0], r[1], r[2], r[3]);
-                        } else if (mirror) {
+                        }
+                        if (!last) {
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                uint32_t l[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float2 h = unpack_half2(o[p][i]);
+                                    l[i] = pack_half2(x[p * 8 + 2 * i] - h.x, x[p * 8 + 2 * i + 1] - h.y);
+                                }
+                                st_shared_v4(st1 + at(hp * 4 + p), l[0], l[1], l[2], l[3]);
+                            }
+                        }
+                    } else {
+                        if (t.prod == 1) {
+                            uint4 u[4];
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) u[p] = ld_shared_v4(st0 + at(hp * 4 + p));
+#pragma unroll
+                            for (int p = 0; p < 4; ++p) {
+                                const uint32_t uu[4] = {u[p].x, u[p].y, u[p].z, u[p].w};
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float2 f = unpack_half2(uu[i]);
+                                    o[p][i] = pack_half2(fmaf(g.b, f.x, quad * x[p * 8 + 2 * i]),
+                                                         fmaf(g.b, f.y, quad * x[p * 8 + 2 * i + 1]));
+                                }
+                            }
+                        } else {
+#pragma unroll
+                            for (int p = 0; p < 4; ++p)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    o[p][i] = pack_half2(x[p * 8 + 2 * i] * g.gram_scale, x[p * 8 + 2 * i + 1] * g.gram_scale);
+                        }
+                        if (mirror) {
                             // the transposed box: row j (a column here) of 32 values, 64-byte swizzle
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int j = p * 8 + i;
+                            for (int i = 0; i < 32; ++i) {
+                                const int j = hp * 32 + i;
                                 const uint32_t to = st1 + j * 64 + ((((lane >> 3) ^ (j >> 1)) & 3) << 4) + (lane & 7) * 2;
-                                const uint16_t h = static_cast<uint16_t>(o[i >> 1] >> (16 * (i & 1)));
+                                const uint16_t h = static_cast<uint16_t>(o[i >> 3][(i >> 1) & 3] >> (16 * (i & 1)));
                                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(to), "h"(h) : "memory");
                             }
                         }
                     }
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) st_shared_v4(st0 + at(hp * 4 + p), o[p][0], o[p][1], o[p][2], o[p][3]);
                 }
                 if (last) {
                     // rows leave 16 bytes a lane, eight lanes a row; sizes that are no multiple of 8 value by value
@@ -425,26 +459,36 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                     }
                 }
             }
-            if (ok && !last && lane == 0) {
-                // this warp's part of the tile is in memory: count it
-                bulk_wait_all();
-                fence_proxy_async();
-                add_release_gpu(g.done + t.b, 1);
+            if (ok && !last) {
+                // the tile is in memory once every warp's stores are (a completed bulk store is visible to its
+                // thread): one thread counts it for all
+                int good = 1;
+                if (lane == 0) {
+                    bulk_wait_all();
+                    mbar_arrive(&sm.stored);
+                    if (ew == 0) {
+                        good = mbar_wait(&sm.stored, tiles & 1, kOrthoWaitNs);
+                        if (good) add_release_gpu(g.done + t.b, 1);
+                    }
+                }
+                ++tiles;
+                if (!__shfl_sync(0xffffffffu, good, 0)) { fail(); break; }
             }
         }
     }
 
     if (warp >= 4 && lane == 0) bulk_wait_all();
     tc_fence_before();
-    cluster_sync();      // neither CTA leaves while the leader's MMAs may read the other's shared memory
+    // neither CTA of a pair leaves while the leader's MMAs may read the other's shared memory
+    if constexpr (PAIR) cluster_sync(); else __syncthreads();
     if (sm.abort_flag) {
         const uint64_t t0 = globaltimer_ns();
         while (globaltimer_ns() - t0 < 200000) __nanosleep(1000);   // copies and MMAs in flight land
     }
-    cluster_sync();
+    if constexpr (PAIR) cluster_sync(); else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        tmem_dealloc_pair(tmem, 512);
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, 512); else tmem_dealloc(tmem, 512);
     }
 }
 
@@ -513,6 +557,8 @@ ortho_norm_kernel(const void* __restrict__ G, int M, int N, int interleaved, dou
     __shared__ double scratch[kNormThreads / 32];
     const int m = blockIdx.y;
     const int64_t n = static_cast<int64_t>(M) * N;
+    dependents_may_launch();
+    wait_for_producers();
     if (blockIdx.x == 0 && threadIdx.x == 0) done[m] = 0;
     double s = 0.0;
     for (int64_t e = (static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x) * kNormVals; e < n;
@@ -533,6 +579,7 @@ ortho_convert_kernel(const void* __restrict__ G, int M, int N, int ldx, int inte
     __shared__ double scratch[kNormThreads / 32];
     const int m = blockIdx.y;
     const int64_t n = static_cast<int64_t>(M) * N;
+    wait_for_producers();
     double s = 0.0;
     for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kNormThreads) s += part[static_cast<int64_t>(m) * gridDim.x + i];
     s = block_sum_f64(s, scratch);
@@ -570,7 +617,7 @@ ortho_convert_kernel(const void* __restrict__ G, int M, int N, int ldx, int inte
 // A wave holds enough matrices to give every CTA pair a tile of the symmetric products, twice over, and never
 // fewer than two (one fills the other's waits); a batch is cut into equal waves that use the workspace in turn.
 int wave_of(int mats, int M, int N, int interleaved) {
-    const int nb = (std::min(M, N) + kOT - 1) / kOT, ns = nb * (nb + 1) / 2;
+    const int nb = (std::min(M, N) + 255) / 256, ns = nb * (nb + 1) / 2;
     const int most = std::max(2, (148 + ns - 1) / ns);
     const int waves = (mats + most - 1) / most;
     int w = (mats + waves - 1) / waves;
@@ -654,52 +701,71 @@ bool coefficients_ok(int steps, float a, float b, float c) {
     return true;
 }
 
+// Tiles of the widest product (the update) of one matrix.
+template <bool PAIR>
+int tiles_of(int M, int N) {
+    constexpr int kEdge = PAIR ? 256 : 128;
+    return ((M + kEdge - 1) / kEdge) * ((N + kEdge - 1) / kEdge);
+}
+
+// Pair tiles (256 x 256) need half the L2 traffic a product; 128 x 128 tiles of single CTAs quarter a tile's latency
+// and spread few tiles over all SMs. Measured on a B200 (us, single / pair), by the update's pair tiles of a wave:
+// 2 (256 x 512) 95 / 120, 16 (1024 x 1024) 147 / 185, 32 (16 of 256 x 512) 105 / 126, 32 (1024 x 2048) 179 / 212,
+// 64 (2048 x 2048) 290 / 273, 128 (4 of 1024 x 2048) 258 / 246, 128 (2048 x 4096) 459 / 396, 512 (4 of 4096 x 2048)
+// 1570 / 1061.
+bool use_pairs(int mats, int M, int N) { return static_cast<int64_t>(mats) * tiles_of<true>(M, N) >= 56; }
+
 template <bool F32>
 cudaError_t launch_prepare(const void* G, int mats, const OrthoArgs& g, const OrthoWs& w, double eps, double xscale,
                            cudaStream_t s) {
-    const dim3 grid(norm_blocks(static_cast<int64_t>(g.M) * g.N), mats);
+    const dim3 grid(norm_blocks(static_cast<int64_t>(g.M) * g.N), mats), block(kNormThreads);
     const int ldx = (g.N + 7) / 8 * 8;
-    if (g.N % 8 == 0) {
-        ortho_norm_kernel<F32, true><<<grid, kNormThreads, 0, s>>>(G, g.M, g.N, g.interleaved, w.part, w.done);
-        ortho_convert_kernel<F32, true><<<grid, kNormThreads, 0, s>>>(G, g.M, g.N, ldx, g.interleaved, w.part, eps, xscale, w.hi[0], w.lo);
-    } else {
-        ortho_norm_kernel<F32, false><<<grid, kNormThreads, 0, s>>>(G, g.M, g.N, g.interleaved, w.part, w.done);
-        ortho_convert_kernel<F32, false><<<grid, kNormThreads, 0, s>>>(G, g.M, g.N, ldx, g.interleaved, w.part, eps, xscale, w.hi[0], w.lo);
-    }
-    return cudaGetLastError();
+    const bool vec = g.N % 8 == 0;
+    const cudaError_t err = launch_dependent(vec ? ortho_norm_kernel<F32, true> : ortho_norm_kernel<F32, false>, grid, block, 0, s,
+                                             G, g.M, g.N, g.interleaved, w.part, w.done);
+    if (err != cudaSuccess) return err;
+    return launch_dependent(vec ? ortho_convert_kernel<F32, true> : ortho_convert_kernel<F32, false>, grid, block, 0, s, G, g.M,
+                            g.N, ldx, g.interleaved, w.part, eps, xscale, w.hi[0], w.lo);
 }
 
+template <bool PAIR>
 cudaError_t launch_steps(const OrthoMaps& maps, const OrthoArgs& g, int num_sms, cudaStream_t s) {
+    auto kern = ortho_steps_kernel<PAIR>;
     const size_t smem = sizeof(SmemO) + 1024;
-    cudaError_t err = cudaFuncSetAttribute(ortho_steps_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeCooperative;      // blocks wait on one another: all of them or none
-    attr[1].val.cooperative = 1;
+    attr[0].id = cudaLaunchAttributeCooperative;      // blocks wait on one another: all of them or none
+    attr[0].val.cooperative = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.blockDim = dim3(kOThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    static int clusters[64] = {0};
-    int dev = 0;
-    if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    int n = __atomic_load_n(&clusters[dev], __ATOMIC_RELAXED);
-    if (n == 0) {
-        cfg.gridDim = dim3(2 * (num_sms / 2));
-        if ((err = cudaOccupancyMaxActiveClusters(&n, ortho_steps_kernel, &cfg)) != cudaSuccess) return err;
-        if (n <= 0) return cudaErrorInvalidConfiguration;
-        __atomic_store_n(&clusters[dev], n, __ATOMIC_RELAXED);
+    int units = num_sms;                              // blocks, or pairs, that fit on the device at once
+    if constexpr (PAIR) {
+        static int clusters[64] = {0};
+        int dev = 0;
+        if ((err = cudaGetDevice(&dev)) != cudaSuccess) return err;
+        if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+        units = __atomic_load_n(&clusters[dev], __ATOMIC_RELAXED);
+        if (units == 0) {
+            cfg.gridDim = dim3(2 * (num_sms / 2));
+            cfg.attrs = attr + 1;
+            cfg.numAttrs = 1;
+            if ((err = cudaOccupancyMaxActiveClusters(&units, kern, &cfg)) != cudaSuccess) return err;
+            if (units <= 0) return cudaErrorInvalidConfiguration;
+            __atomic_store_n(&clusters[dev], units, __ATOMIC_RELAXED);
+        }
     }
-    cfg.gridDim = dim3(2 * n);
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, ortho_steps_kernel, maps, g);
+    units = static_cast<int>(std::min<int64_t>(units, static_cast<int64_t>(g.mats) * tiles_of<PAIR>(g.M, g.N)));
+    cfg.gridDim = dim3(PAIR ? 2 * units : units);
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, maps, g);
 }
 
 bool ptr_ok(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -768,7 +834,8 @@ moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const v
         if (!ok) return MOE_ERR_CUDA;
         cudaError_t err = g_type == MOE_TYPE_FP32 ? launch_prepare<true>(gw, g.mats, g, w, eps, xscale, s)
                                                   : launch_prepare<false>(gw, g.mats, g, w, eps, xscale, s);
-        if (err == cudaSuccess) err = launch_steps(maps, g, num_sms, s);
+        if (err == cudaSuccess)
+            err = use_pairs(g.mats, M, N) ? launch_steps<true>(maps, g, num_sms, s) : launch_steps<false>(maps, g, num_sms, s);
         if (err != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;
