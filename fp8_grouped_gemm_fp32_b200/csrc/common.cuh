@@ -141,6 +141,12 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 // Waits until every committed bulk store of this thread has finished reading shared memory.
 __device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 
+// The same for all but the newest N.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
 // Waits until every committed bulk store of this thread has completed.
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
@@ -324,6 +330,28 @@ __device__ __forceinline__ void umma_f16(uint32_t d_tmem, uint64_t a_desc, uint6
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+
+// The same in a run of MMAs with one A operand: the first fills the tensor core's A buffer, the others use it
+// (the last one frees it), so A is read from shared memory once.
+enum class KeepA { kFill, kUse, kLast };
+#define MOE_UMMA_KEEP(GROUP, OP)                                                                             \
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"                                          \
+                 "tcgen05.mma.cta_group::" GROUP ".kind::f16.collector::a::" OP " [%0], %1, %2, %3, p;\n\t}" \
+                 ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory")
+template <bool PAIR, KeepA KEEP>
+__device__ __forceinline__ void umma_f16_keep(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                              uint32_t accumulate) {
+    if constexpr (PAIR) {
+        if constexpr (KEEP == KeepA::kFill) MOE_UMMA_KEEP("2", "fill");
+        else if constexpr (KEEP == KeepA::kUse) MOE_UMMA_KEEP("2", "use");
+        else MOE_UMMA_KEEP("2", "lastuse");
+    } else {
+        if constexpr (KEEP == KeepA::kFill) MOE_UMMA_KEEP("1", "fill");
+        else if constexpr (KEEP == KeepA::kUse) MOE_UMMA_KEEP("1", "use");
+        else MOE_UMMA_KEEP("1", "lastuse");
+    }
+}
+#undef MOE_UMMA_KEEP
 
 // ------------------------------------------------------------------ CTA pairs (cluster of two)
 // Two CTAs of a cluster share one tensor-core operation: tcgen05.mma.cta_group::2 issued by the pair's

@@ -262,6 +262,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                 const bool b_mn = (t.prod == 0 && sh.tall) || (t.prod == 2 && !sh.tall);
                 const int K = t.prod == 0 ? sh.l : sh.s;
                 const uint32_t idesc = f16_idesc(kEdge, kEdge, false, a_mn, b_mn);
+                const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
                 const uint32_t buf = ti & 1, d = tmem + buf * kEdge;
                 if (!mbar_wait(&sm.tempty[buf], ((ti >> 1) & 1) ^ 1, kOrthoWaitNs)) { fail(); break; }
                 tc_fence_after();
@@ -269,12 +270,12 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                     const int s = it % kOStages;
                     if (!mbar_wait(&sm.full[s], (it / kOStages) & 1, kOrthoWaitNs)) { fail(); ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(sm.a[s]), b0 = smem_u32(sm.b[s]);
+                    // 16 K values on (the descriptors hold address / 16): 32 bytes in a K-major row, 16 rows of 128 bytes
+                    // of an MN-major box
+                    uint64_t da = a_mn ? sw128_mnmajor_desc(smem_u32(sm.a[s]), kOBox) : sw128_kmajor_desc(smem_u32(sm.a[s]));
+                    uint64_t db = b_mn ? sw128_mnmajor_desc(smem_u32(sm.b[s]), kOBox) : sw128_kmajor_desc(smem_u32(sm.b[s]));
 #pragma unroll
-                    for (int kk = 0; kk < kOK / 16; ++kk) {
-                        // 16 K values: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major box
-                        const uint64_t da = a_mn ? sw128_mnmajor_desc(a0 + kk * 2048, kOBox) : sw128_kmajor_desc(a0 + kk * 32);
-                        const uint64_t db = b_mn ? sw128_mnmajor_desc(b0 + kk * 2048, kOBox) : sw128_kmajor_desc(b0 + kk * 32);
+                    for (int kk = 0; kk < kOK / 16; ++kk, da += a_step, db += b_step) {
                         if constexpr (PAIR) umma_f16_pair(d, da, db, idesc, k0 + kk > 0);
                         else umma_f16(d, da, db, idesc, k0 + kk > 0);
                     }
@@ -478,6 +479,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
     }
 
     if (warp >= 4 && lane == 0) bulk_wait_all();
+    __syncwarp();
     tc_fence_before();
     // neither CTA of a pair leaves while the leader's MMAs may read the other's shared memory
     if constexpr (PAIR) cluster_sync(); else __syncthreads();

@@ -1,23 +1,23 @@
 // A dense gradient of the router's logits through its linear layer (logits = x W_g^T + b):
 //   dx = dx0 + dl W_g [T, H] bf16,  dWg = dWg0 + dl^T x [E, H] fp32,  db = db0 + sum_t dl.
 //
-// 4 T H E multiply-adds x 2 against x read once, dx0 read and dx written: at 256 experts the products and the
-// traffic cost about the same, so both products run on the tensor cores and dx is bound by its own traffic.
+// 4 T H E flops against x read once, dx0 read and dx written: at 256 experts the products and the traffic cost
+// about the same, so both products run on the tensor cores and dx is bound by its own traffic.
 //
 //  1. router_prep_w_kernel, router_prep_dl_kernel: fp16 copies for dx, each expert's W_g row scaled by a power
 //     of two so that its largest entry lies in [512, 1024), that power moved into dl, then each token's dl row
 //     scaled likewise (undone in dx's epilogue); dl in three bf16 parts (8 + 8 + 8 bits, all of fp32) for dWg;
 //     partial column sums of dl for db.
-//  2. router_dx_kernel: one fp16 product. fp16 keeps 11 bits, so dx is off by about an eighth of the step it
-//     is rounded with; bf16 parts would need three products for that. A CTA keeps its W_g panel (all experts x
-//     256 columns, or 128 above 256 experts) in shared memory and streams token tiles through it: without that
-//     the panels alone would cost more L2 traffic than dx does HBM traffic.
-//  3. router_dw_kernel: the transposed product, x^T (rows h) by the parts of dl, both operands read as they
-//     lie in memory (MN-major), so E is the MMA's N and a few experts cost little. The tensor cores drop bits
-//     when they add to a long sum, so every 128 tokens the sum moves from tensor memory into fp32 registers.
-//     The (tile, 128 tokens) units are dealt out evenly; a CTA (pair) leaves one partial tile per tile it
-//     touched, at index tile + its own index (unique: both only rise), and
-//  4. router_finish_kernel adds the partial tiles in order, and db. No float atomics: results repeat.
+//  2. router_products_kernel, first dx: one fp16 product. fp16 keeps 11 bits, so dx is off by about an eighth
+//     of the step it is rounded with; bf16 parts would need three products for that. A CTA keeps its W_g panel
+//     (all experts x 256 columns) in shared memory and streams token tiles through it (without that the panels
+//     alone would cost more L2 traffic than dx does HBM traffic), the next tile's dx0 loading meanwhile.
+//     Then dWg: the transposed product, x^T (rows h) by the parts of dl, both operands read as they lie in
+//     memory (MN-major), so E is the MMA's N and a few experts cost little. The tensor cores drop bits when they
+//     add to a long sum, so every 128 tokens the sum moves from tensor memory into fp32 registers. The work of
+//     either product is dealt out evenly as one run of units a CTA (or pair); for dWg it leaves one partial tile
+//     per tile it touched, at index tile + its own index (unique: both only rise), and
+//  3. router_finish_kernel adds the partial tiles in order, and db. No float atomics: results repeat.
 #include <cmath>
 
 #include <algorithm>
@@ -36,7 +36,7 @@ namespace {
 constexpr uint64_t kRbWaitNs = 4000000000ull;
 constexpr int kRbBox = 64 * 64 * 2;            // a 64 x 64 operand box: 8 KB
 constexpr int kRbThreads = 384;                // TMA, MMA, two idle warps, eight epilogue warps
-constexpr int kPrepTokens = 32;                // tokens of a dl preparation block
+constexpr int kPrepTokens = 32;                // tokens of a dl preparation block, four a warp
 constexpr int kRbChunk = 128;                  // tokens summed in tensor memory before promotion
 
 __device__ __forceinline__ uint16_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
@@ -54,7 +54,10 @@ __global__ void __launch_bounds__(256)
 router_prep_w_kernel(const float* __restrict__ Wg, int H, uint16_t* __restrict__ wh, float* __restrict__ wscale) {
     __shared__ float sm[8];
     const int64_t base = static_cast<int64_t>(blockIdx.x) * H;
+    dependents_may_launch();
+    wait_for_producers();
     float m = 0.0f;
+#pragma unroll 4
     for (int h = threadIdx.x * 4; h < H; h += 1024) {
         const float4 f = *reinterpret_cast<const float4*>(Wg + base + h);
         m = fmaxf(m, fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
@@ -66,6 +69,7 @@ router_prep_w_kernel(const float* __restrict__ Wg, int H, uint16_t* __restrict__
     for (int i = 0; i < 8; ++i) m = fmaxf(m, sm[i]);
     const float2 sc = pow2_scale(m);
     if (threadIdx.x == 0) wscale[blockIdx.x] = sc.y;
+#pragma unroll 4
     for (int h = threadIdx.x * 4; h < H; h += 1024) {
         const float4 f = *reinterpret_cast<const float4*>(Wg + base + h);
         const __half2 a = __floats2half2_rn(f.x * sc.x, f.y * sc.x), b = __floats2half2_rn(f.z * sc.x, f.w * sc.x);
@@ -75,55 +79,84 @@ router_prep_w_kernel(const float* __restrict__ Wg, int H, uint16_t* __restrict__
 }
 
 // dl rows -> fp16 (times the experts' inverse scales, then scaled per token; tscale[t] undoes it), three bf16
-// parts [3][T][ld], and the block's column sums. A warp takes a token at a time, lane j experts j, j + 32, ...
+// parts [3][T][ld], and the block's column sums. A warp takes a token at a time; Q groups of four experts a lane
+// (16-byte reads where E is a multiple of 4).
+template <int Q, bool VEC>
 __global__ void __launch_bounds__(256)
 router_prep_dl_kernel(const float* __restrict__ dl, const float* __restrict__ wscale, int T, int E, int ld,
                       uint16_t* __restrict__ dlh, float* __restrict__ tscale, uint16_t* __restrict__ parts,
                       float* __restrict__ dbpart) {
-    constexpr int V = kMaxE / 32;
-    __shared__ float sm[8][kMaxE];
+    __shared__ float sm[8][Q * 128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = blockIdx.x * kPrepTokens, t1 = min(t0 + kPrepTokens, T);
+    const int t0 = blockIdx.x * kPrepTokens + warp, t1 = min((static_cast<int>(blockIdx.x) + 1) * kPrepTokens, T);
     const int64_t plane = static_cast<int64_t>(T) * ld;
-    const int nv = (E + 31) / 32;
-    float sum[V], w[V];
+    auto load = [&](int t, float (&v)[4 * Q]) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
+        for (int q = 0; q < Q; ++q) {
+            const int e = 4 * (lane + 32 * q);
+            const float* p = dl + static_cast<int64_t>(t) * E + e;
+            if constexpr (VEC) {
+                float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (t < t1 && e < E) f = *reinterpret_cast<const float4*>(p);
+                v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[4 * q + i] = t < t1 && e + i < E ? p[i] : 0.0f;
+            }
+        }
+    };
+    dependents_may_launch();
+    wait_for_producers();
+    float v[4 * Q], sum[4 * Q], w[4 * Q];
+    load(t0, v);
+#pragma unroll
+    for (int i = 0; i < 4 * Q; ++i) {
+        const int e = 4 * (lane + 32 * (i / 4)) + i % 4;
         sum[i] = 0.0f;
-        w[i] = i < nv && lane + 32 * i < E ? wscale[lane + 32 * i] : 0.0f;
+        w[i] = e < E ? wscale[e] : 0.0f;
     }
-    for (int t = t0 + warp; t < t1; t += 8) {
-        float v[V];
+    for (int t = t0; t < t1; t += 8) {
+        float nx[4 * Q];
+        load(t + 8, nx);
         float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            v[i] = i < nv && e < E ? dl[static_cast<int64_t>(t) * E + e] : 0.0f;
+        for (int i = 0; i < 4 * Q; ++i) {
             sum[i] += v[i];
             m = fmaxf(m, fabsf(v[i] * w[i]));
         }
         const float2 sc = pow2_scale(warp_max(m));
         if (lane == 0) tscale[t] = sc.y;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane + 32 * i;
-            if (i < nv && e < E) {
+        for (int q = 0; q < Q; ++q) {
+            const int e = 4 * (lane + 32 * q);
+            if (e < E) {
+                // rows are padded to a multiple of 8 experts: whole 8-byte stores, zeros behind the last
                 const int64_t at = static_cast<int64_t>(t) * ld + e;
-                dlh[at] = __half_as_ushort(__float2half_rn(v[i] * w[i] * sc.x));
-                float r = v[i];
+                uint16_t h[4], b[3][4];
 #pragma unroll
-                for (int p = 0; p < 3; ++p) {
-                    const uint16_t b = bf16_bits(r);
-                    parts[p * plane + at] = b;
-                    // what is left is exact; an infinite or NaN value is carried by its first part alone
-                    r = fabsf(r) <= 3.0e38f ? r - bf16_bits_to_f32(b) : 0.0f;
+                for (int i = 0; i < 4; ++i) {
+                    h[i] = __half_as_ushort(__float2half_rn(v[4 * q + i] * w[4 * q + i] * sc.x));
+                    float r = v[4 * q + i];
+#pragma unroll
+                    for (int p = 0; p < 3; ++p) {
+                        b[p][i] = bf16_bits(r);
+                        // what is left is exact; an infinite or NaN value is carried by its first part alone
+                        r = fabsf(r) <= 3.0e38f ? r - bf16_bits_to_f32(b[p][i]) : 0.0f;
+                    }
                 }
+                auto put = [](uint16_t* dst, const uint16_t (&u)[4]) {
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(u[0] | static_cast<uint32_t>(u[1]) << 16, u[2] | static_cast<uint32_t>(u[3]) << 16);
+                };
+                put(dlh + at, h);
+#pragma unroll
+                for (int p = 0; p < 3; ++p) put(parts + p * plane + at, b[p]);
             }
         }
+#pragma unroll
+        for (int i = 0; i < 4 * Q; ++i) v[i] = nx[i];
     }
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-        if (lane + 32 * i < E) sm[warp][lane + 32 * i] = sum[i];
+    for (int i = 0; i < 4 * Q; ++i) sm[warp][4 * (lane + 32 * (i / 4)) + i % 4] = sum[i];
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += 256) {
         float s = 0.0f;
@@ -133,205 +166,82 @@ router_prep_dl_kernel(const float* __restrict__ dl, const float* __restrict__ ws
     }
 }
 
-// ---------------------------------------------------------------- 2. dx
-// PN columns of H a CTA, KB = 64-expert blocks of the panel (PN x KB x 128 bytes <= 128 KB).
-template <int PN>
-struct SmemX {
-    static constexpr int kStages = 2;
-    static constexpr int kPanelBlocks = 4 * 256 / PN;
-    uint8_t w[kPanelBlocks][PN * 128];
-    uint8_t a[kStages][2 * kRbBox];
-    uint8_t stage[8][PN / 128][4096];          // per epilogue warp: 32 rows x 64 columns, bf16
-    uint64_t wfull;
-    uint64_t full[kStages];
-    uint64_t empty[kStages];
-    uint64_t tfull[2];
-    uint64_t tempty[2];
-    uint64_t eload[8];
-    uint32_t tmem_base;
-    volatile int abort_flag;
-};
-
-template <int PN, bool BASE>
-__global__ void __launch_bounds__(kRbThreads, 1)
-router_dx_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant__ CUtensorMap tm_w,
-                 const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out,
-                 const float* __restrict__ tscale, int T, int H, int E, int panels, int* status) {
-    extern __shared__ uint8_t smem_raw[];
-    using SX = SmemX<PN>;
-    SX& sm = *reinterpret_cast<SX*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int KB = (E + 63) / 64;
-    const int panel = blockIdx.x % panels, n0 = panel * PN;
-    // the CTAs of a panel take its token tiles in turn
-    const int first = blockIdx.x / panels, step = (gridDim.x - panel + panels - 1) / panels;
-    const int tiles = (T + 127) / 128;
-    if (threadIdx.x == 0) {
-        mbar_init(&sm.wfull, 1);
-        for (int s = 0; s < SX::kStages; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&sm.tfull[i], 1); mbar_init(&sm.tempty[i], 8); }
-        for (int i = 0; i < 8; ++i) mbar_init(&sm.eload[i], 1);
-        sm.abort_flag = 0;
-        fence_mbar_init();
-    }
-    if (warp == 1) { tmem_alloc(&sm.tmem_base, 512); tmem_relinquish(); }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = sm.tmem_base;
-    auto fail = [&]() { set_status(status, kStatusTimeout); sm.abort_flag = 1; };
-
-    if (warp == 0) {
-        if (lane == 0) {
-            if (first < tiles) {
-                mbar_arrive_expect_tx(&sm.wfull, KB * PN * 128);
-                for (int kb = 0; kb < KB; ++kb)
-                    for (int i = 0; i < PN / 64; ++i)
-                        tma_load_2d(sm.w[kb] + i * kRbBox, &tm_w, &sm.wfull, n0 + 64 * i, kb * 64);
-            }
-            uint32_t it = 0;
-            bool ok = true;
-            for (int tile = first; ok && tile < tiles; tile += step)
-                for (int kb = 0; kb < KB; ++kb, ++it) {
-                    const int s = it % SX::kStages;
-                    if (!mbar_wait(&sm.empty[s], ((it / SX::kStages) & 1) ^ 1, kRbWaitNs)) { fail(); ok = false; break; }
-                    mbar_arrive_expect_tx(&sm.full[s], 2 * kRbBox);
-                    tma_load_2d(sm.a[s], &tm_dl, &sm.full[s], kb * 64, tile * 128);
-                }
-        }
-    } else if (warp == 1) {
-        if (lane == 0 && first < tiles) {
-            uint32_t it = 0, ti = 0;
-            const uint32_t idesc = f16_idesc(128, PN, false, false, true);
-            bool ok = mbar_wait(&sm.wfull, 0, kRbWaitNs);
-            if (!ok) fail();
-            for (int tile = first; ok && tile < tiles && !sm.abort_flag; tile += step, ++ti) {
-                const uint32_t buf = ti & 1, d = tmem + buf * 256;
-                if (!mbar_wait(&sm.tempty[buf], ((ti >> 1) & 1) ^ 1, kRbWaitNs)) { fail(); break; }
-                for (int kb = 0; kb < KB; ++kb, ++it) {
-                    const int s = it % SX::kStages;
-                    if (!mbar_wait(&sm.full[s], (it / SX::kStages) & 1, kRbWaitNs)) { fail(); ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t a0 = smem_u32(sm.a[s]), b0 = smem_u32(sm.w[kb]);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk)
-                        umma_f16(d, sw128_kmajor_desc(a0 + kk * 32), sw128_mnmajor_desc(b0 + kk * 2048, kRbBox), idesc,
-                                 kb + kk > 0);
-                    umma_commit(&sm.empty[s]);
-                }
-                if (ok) umma_commit(&sm.tfull[buf]);
-            }
-        }
-    } else if (warp >= 4) {
-        constexpr int kSubs = PN / 128;         // 64-column boxes of a warp: its half of the panel
-        const int ew = warp - 4, q = warp & 3, half = ew >> 2;
-        uint32_t ti = 0;
-        for (int tile = first; tile < tiles; tile += step, ++ti) {
-            if (sm.abort_flag) break;
-            const uint32_t buf = ti & 1;
-            const int row0 = tile * 128 + q * 32, col0 = n0 + half * (PN / 2);
-            const float sc = row0 + lane < T ? tscale[row0 + lane] : 0.0f;
-            if (lane == 0) {
-                bulk_wait_read_all();
-                if (BASE) {
-                    mbar_arrive_expect_tx(&sm.eload[ew], kSubs * 4096);
-                    for (int i = 0; i < kSubs; ++i)
-                        tma_load_2d(sm.stage[ew][i], &tm_in, &sm.eload[ew], col0 + 64 * i, row0);
-                }
-            }
-            __syncwarp();
-            if (!mbar_wait(&sm.tfull[buf], (ti >> 1) & 1, kRbWaitNs)) { fail(); break; }
-            tc_fence_after();
-            if (BASE && !mbar_wait(&sm.eload[ew], ti & 1, kRbWaitNs)) { fail(); break; }
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * (PN / 2);
-#pragma unroll
-            for (int i = 0; i < kSubs; ++i) {
-                float v[2][32];
-                tmem_ld32(taddr + 64 * i, v[0]);
-                tmem_ld32(taddr + 64 * i + 32, v[1]);
-                tmem_ld_wait();
-                if (i == kSubs - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm.tempty[buf]);
-                }
-                const uint32_t st = smem_u32(sm.stage[ew][i]) + lane * 128;
-#pragma unroll
-                for (int p = 0; p < 8; ++p) {
-                    const uint32_t at = st + ((p ^ (lane & 7)) << 4);
-                    uint32_t b[4] = {0, 0, 0, 0}, o[4];
-                    if (BASE)
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]) : "r"(at) : "memory");
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const int c = (p & 3) * 8 + 2 * j;
-                        const float x = fmaf(v[p >> 2][c], sc, __uint_as_float(b[j] << 16));
-                        const float y = fmaf(v[p >> 2][c + 1], sc, __uint_as_float(b[j] & 0xffff0000u));
-                        const __nv_bfloat162 r = __floats2bfloat162_rn(x, y);
-                        o[j] = *reinterpret_cast<const uint32_t*>(&r);
-                    }
-                    st_shared_v4(at, o[0], o[1], o[2], o[3]);
-                }
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                if (row0 < T)
-                    for (int i = 0; i < kSubs; ++i)
-                        if (col0 + 64 * i < H) tma_store_2d(&tm_out, sm.stage[ew][i], col0 + 64 * i, row0);
-                bulk_commit();
-            }
-        }
-    }
-    if (warp >= 4 && lane == 0) bulk_wait_all();
-    tc_fence_before();
-    __syncthreads();
-    if (sm.abort_flag) {
-        const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 200000) __nanosleep(1000);   // copies and MMAs in flight land
-    }
-    __syncthreads();
-    if (warp == 1) { tc_fence_after(); tmem_dealloc(tmem, 512); }
-}
-
-// ---------------------------------------------------------------- 3. partial tiles of dWg^T
-// PAIR: 256 rows of H x 256 experts by a CTA pair (128 of each in either CTA); otherwise 128 rows x up to 128
-// experts by one CTA. Unit u of U = tiles * chunks is chunk u % chunks of tile u / chunks; group g of G takes
-// units [g U / G, (g + 1) U / G).
-constexpr int kDwStages = 3;
+// ---------------------------------------------------------------- 2. the products
+// PAIR (above 128 experts): CTA pairs, 256 tokens x 256 columns of dx, 256 columns x 256 experts of dWg. The
+// operand that both halves of a tile need is then held once a pair: 64 KB a stage cross from L2 where single CTAs
+// would load 112 KB for the same MMAs. Otherwise single CTAs, 128 x 256 and 128 x 128. KB: 64-expert blocks of the
+// W_g panel, AS: those of the tokens' ring, NB: dx0 / dx boxes an epilogue warp holds (what the panel leaves room for).
+// Units are dealt out as runs: group g of G takes [g U / G, (g + 1) U / G).
+constexpr int kDwStages = 5;                                               // barriers; the ring's depth goes by E
+constexpr int kDwRing = 24 * kRbBox;                                       // its bytes: 192 KB
 constexpr int kDwRegsLow = 40, kDwRegsHigh = 232;                          // as in the grouped GEMM:
 constexpr int kDwRegsSplit = 128 * kDwRegsLow + 256 * kDwRegsHigh;        // what the launch must have allocated
 
-struct SmemW {
-    uint8_t x[kDwStages][2 * kRbBox];          // 64 tokens x 128 columns of x
-    uint8_t d[kDwStages][3][2 * kRbBox];       // 64 tokens x 128 experts of each part
-    uint64_t full[kDwStages];
-    uint64_t empty[kDwStages];
-    uint64_t tfull[2];
-    uint64_t tempty[2];
+template <bool PAIR, int KB, int AS, int NB>
+struct SmemDx {
+    uint8_t w[KB][PAIR ? 2 * kRbBox : 4 * kRbBox];     // the CTA's 128 (of a pair's 256) or 256 panel columns
+    uint8_t a[AS][2 * kRbBox];                         // 64 experts of 128 tokens
+    uint8_t stage[8][NB][4096];                        // per epilogue warp: 32 rows x 64 columns, bf16
+};
+// dWg's ring: a stage is 64 tokens x 128 columns of x (2 boxes), then 64 tokens x 64 experts of each part (1 or 2
+// boxes a part): 5 boxes where E <= 64, else 8.
+struct SmemDw {
+    uint8_t ring[kDwRing + kRbBox];
+};
+template <bool PAIR, int KB, int AS, int NB>
+struct SmemP {
+    union {
+        SmemDx<PAIR, KB, AS, NB> dx;
+        SmemDw dw;
+    };
+    uint64_t wfull, wempty;
+    uint64_t afull[AS], aempty[AS];
+    uint64_t eload[8][NB];
+    uint64_t full[kDwStages], empty[kDwStages];
+    uint64_t tfull[2][2], tempty[2][2];        // [product][accumulator]
     uint32_t tmem_base;
     volatile int abort_flag;
 };
 
-__host__ __device__ __forceinline__ int64_t unit_start(int64_t U, int G, int g) { return U * g / G; }
+__host__ __device__ __forceinline__ int unit_start(int U, int G, int g) { return static_cast<int>(static_cast<int64_t>(U) * g / G); }
 // The group that holds unit u: the largest g with unit_start(g) <= u.
-__device__ __forceinline__ int group_of(int64_t U, int G, int64_t u) { return static_cast<int>(((u + 1) * G + U - 1) / U - 1); }
+inline int group_of(int U, int G, int u) { return static_cast<int>((static_cast<int64_t>(u + 1) * G + U - 1) / U - 1); }
 
-template <bool PAIR>
+struct RouterArgs {
+    int T, H, E;
+    int has_base;
+    int Gx, Gw;               // groups that share dx's units, dWg's units
+    int etiles;               // expert tiles of dWg
+    int Ux, Uw;
+    const float* tscale;
+    float* part;
+    int* status;
+};
+
+template <bool PAIR, int KB, int AS, int NB>
 __global__ void __launch_bounds__(kRbThreads, 1)
-router_dw_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_d, int T, int H,
-                 int E, int etiles, int64_t U, int G, float* __restrict__ part, int* status) {
-    constexpr int kRows = PAIR ? 256 : 128, kCols = PAIR ? 256 : 128;
+router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant__ CUtensorMap tm_w,
+                       const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out,
+                       const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_d,
+                       const RouterArgs g) {
+    constexpr int kTok = PAIR ? 256 : 128;                      // tokens of a dx tile
+    constexpr int kRows = PAIR ? 256 : 128, kCols = PAIR ? 256 : 128;   // dWg tile: columns of x, experts
+    constexpr int kWBoxes = PAIR ? 2 : 4;                       // 64-column boxes of the panel this CTA holds
     extern __shared__ uint8_t smem_raw[];
-    SmemW& sm = *reinterpret_cast<SmemW*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    using SP = SmemP<PAIR, KB, AS, NB>;
+    SP& sm = *reinterpret_cast<SP*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_ctarank() : 0;
     const int grp = PAIR ? static_cast<int>(cluster_id_x()) : static_cast<int>(blockIdx.x);
-    const int chunks = (T + kRbChunk - 1) / kRbChunk;
-    const int64_t u0 = unit_start(U, G, grp), u1 = unit_start(U, G, grp + 1);
     if (threadIdx.x == 0) {
+        mbar_init(&sm.wfull, 1);
+        mbar_init(&sm.wempty, 1);
+        for (int s = 0; s < AS; ++s) { mbar_init(&sm.afull[s], 1); mbar_init(&sm.aempty[s], 1); }
         for (int s = 0; s < kDwStages; ++s) { mbar_init(&sm.full[s], 1); mbar_init(&sm.empty[s], 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(&sm.tfull[i], 1); mbar_init(&sm.tempty[i], PAIR ? 16 : 8); }
+        for (int p = 0; p < 2; ++p)
+            for (int i = 0; i < 2; ++i) { mbar_init(&sm.tfull[p][i], 1); mbar_init(&sm.tempty[p][i], PAIR ? 16 : 8); }
+        for (int i = 0; i < 8; ++i)
+            for (int n = 0; n < NB; ++n) mbar_init(&sm.eload[i][n], 1);
         sm.abort_flag = 0;
         fence_mbar_init();
     }
@@ -339,123 +249,303 @@ router_dw_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
         if constexpr (PAIR) { tmem_alloc_pair(&sm.tmem_base, 512); tmem_relinquish_pair(); }
         else { tmem_alloc(&sm.tmem_base, 512); tmem_relinquish(); }
     }
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tm_dl); prefetch_tensormap(&tm_w); prefetch_tensormap(&tm_in);
+        prefetch_tensormap(&tm_out); prefetch_tensormap(&tm_x); prefetch_tensormap(&tm_d);
+    }
     tc_fence_before();
     if constexpr (PAIR) cluster_sync(); else __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sm.tmem_base;
+    dependents_may_launch();
+    wait_for_producers();
     auto fail = [&]() {
-        set_status(status, kStatusTimeout);
+        set_status(g.status, kStatusTimeout);
         sm.abort_flag = 1;
         if constexpr (PAIR) st_shared_cluster_u32(mapa_shared(smem_u32((const void*)&sm.abort_flag), rank ^ 1u), 1u);
     };
-    const int ebox = PAIR ? 2 : (E + 63) / 64;       // 64-expert boxes of each part a CTA loads
+    auto leader_bar = [&](uint64_t* bar) -> uint32_t { return PAIR ? mapa_shared(smem_u32(bar), 0) : 0u; };
+    auto release = [&](uint64_t* bar) {       // an accumulator buffer, by one lane of an epilogue warp
+        if (PAIR && rank) mbar_arrive_cluster(leader_bar(bar));
+        else mbar_arrive(bar);
+    };
 
+    // ======== dx: unit u = token tile u % ttiles of panel u / ttiles
+    const int ttiles = (g.T + kTok - 1) / kTok, kblocks = (g.E + 63) / 64;
+    const int x0 = grp < g.Gx ? unit_start(g.Ux, g.Gx, grp) : 0, x1 = grp < g.Gx ? unit_start(g.Ux, g.Gx, grp + 1) : 0;
+    // ======== dWg: unit u = 128-token chunk u % chunks of tile u / chunks
+    const int chunks = (g.T + kRbChunk - 1) / kRbChunk;
+    const int u0 = grp < g.Gw ? unit_start(g.Uw, g.Gw, grp) : 0, u1 = grp < g.Gw ? unit_start(g.Uw, g.Gw, grp + 1) : 0;
+    const int ebox = PAIR ? 2 : (g.E + 63) / 64;      // 64-expert boxes of each part a CTA loads
+    const uint32_t depth = ebox == 1 ? 5 : 3, stage_bytes = (2 + 3 * ebox) * kRbBox;
+    const uint32_t part_step = ebox * kRbBox / 16;
+    auto stage_x = [&](uint32_t s) { return sm.dw.ring + s * stage_bytes; };
+    auto stage_d = [&](uint32_t s, int p) { return sm.dw.ring + s * stage_bytes + (2 + p * ebox) * kRbBox; };
+
+    // The products are independent: half of the groups begin with dWg, so that dx's traffic and dWg's products run
+    // beside each other on the GPU. Between the two a group's MMAs are complete (their accumulators were waited
+    // for), and its stores have left shared memory.
+    const int dx_turn = grp & 1;
+    auto turn_over = [&]() {
+        __syncwarp();
+        if constexpr (PAIR) cluster_sync(); else __syncthreads();
+    };
     if (warp < 4) {
         setmaxnreg_dec<kDwRegsLow>();
-        if (warp == 0 && lane == 0) {
-            uint32_t it = 0;
-            bool ok = true;
-            const uint32_t bytes = (PAIR ? 2u : 1u) * (2 + 3 * ebox) * kRbBox;
-            for (int64_t u = u0; ok && u < u1; ++u) {
-                const int tile = static_cast<int>(u / chunks), t0 = static_cast<int>(u - static_cast<int64_t>(tile) * chunks) * kRbChunk;
-                const int h0 = tile / etiles * kRows + static_cast<int>(rank) * 128;
-                const int e0 = tile % etiles * kCols + static_cast<int>(rank) * 128;
-                for (int t = t0; t < min(t0 + kRbChunk, T); t += 64, ++it) {
-                    const int s = it % kDwStages;
-                    if (!mbar_wait(&sm.empty[s], ((it / kDwStages) & 1) ^ 1, kRbWaitNs)) { fail(); ok = false; break; }
-                    if constexpr (PAIR) {
-                        const uint32_t fb = mapa_shared(smem_u32(&sm.full[s]), 0);
-                        if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], bytes);
-                        for (int i = 0; i < 2; ++i) tma_load_3d_pair(sm.x[s] + i * kRbBox, &tm_x, fb, h0 + 64 * i, t, 0);
-                        for (int p = 0; p < 3; ++p)
-                            for (int i = 0; i < 2; ++i) tma_load_3d_pair(sm.d[s][p] + i * kRbBox, &tm_d, fb, e0 + 64 * i, t, p);
-                    } else {
-                        mbar_arrive_expect_tx(&sm.full[s], bytes);
-                        for (int i = 0; i < 2; ++i) tma_load_3d(sm.x[s] + i * kRbBox, &tm_x, &sm.full[s], h0 + 64 * i, t, 0);
-                        for (int p = 0; p < 3; ++p)
-                            for (int i = 0; i < ebox; ++i) tma_load_3d(sm.d[s][p] + i * kRbBox, &tm_d, &sm.full[s], e0 + 64 * i, t, p);
-                    }
-                }
-            }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
-            uint32_t it = 0, ci = 0;
-            bool ok = true;
-            const uint32_t idesc = f16_idesc(kRows, PAIR ? 256 : (E + 15) / 16 * 16, true, true, true);
-            for (int64_t u = u0; ok && u < u1 && !sm.abort_flag; ++u, ++ci) {
-                const int t0 = static_cast<int>(u % chunks) * kRbChunk;
-                const uint32_t buf = ci & 1, d = tmem + buf * 256;
-                if (!mbar_wait(&sm.tempty[buf], ((ci >> 1) & 1) ^ 1, kRbWaitNs)) { fail(); break; }
-                for (int t = t0; t < min(t0 + kRbChunk, T); t += 64, ++it) {
-                    const int s = it % kDwStages;
-                    if (!mbar_wait(&sm.full[s], (it / kDwStages) & 1, kRbWaitNs)) { fail(); ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t a0 = smem_u32(sm.x[s]);
-#pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        const uint32_t b0 = smem_u32(sm.d[s][p]);
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t da = sw128_mnmajor_desc(a0 + kk * 2048, kRbBox);
-                            const uint64_t db = sw128_mnmajor_desc(b0 + kk * 2048, kRbBox);
-                            const uint32_t acc = t > t0 || p + kk > 0;
-                            if constexpr (PAIR) umma_f16_pair(d, da, db, idesc, acc);
-                            else umma_f16(d, da, db, idesc, acc);
+        for (int turn = 0; turn < 2; ++turn) {
+            if (turn == dx_turn) {
+                if (warp == 0 && lane == 0) {
+                    uint32_t it = 0, panels = 0;
+                    int have = -1;
+                    bool ok = !sm.abort_flag;
+                    for (int u = x0; ok && u < x1; ++u) {
+                        const int panel = u / ttiles, tile = u - panel * ttiles;
+                        if (panel != have) {
+                            // the panel before it is no longer read: its last MMAs have committed
+                            if (panels > 0 && !mbar_wait(&sm.wempty, (panels - 1) & 1, kRbWaitNs)) { fail(); break; }
+                            have = panel;
+                            ++panels;
+                            const int c0 = panel * 256 + static_cast<int>(rank) * 128;
+                            if (rank == 0) mbar_arrive_expect_tx(&sm.wfull, (PAIR ? 2u : 1u) * kblocks * kWBoxes * kRbBox);
+                            for (int kb = 0; kb < kblocks; ++kb)
+                                for (int i = 0; i < kWBoxes; ++i) {
+                                    if constexpr (PAIR)
+                                        tma_load_2d_pair(sm.dx.w[kb] + i * kRbBox, &tm_w, leader_bar(&sm.wfull), c0 + 64 * i, kb * 64);
+                                    else
+                                        tma_load_2d(sm.dx.w[kb] + i * kRbBox, &tm_w, &sm.wfull, c0 + 64 * i, kb * 64);
+                                }
+                        }
+                        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                            const int s = it % AS;
+                            if (!mbar_wait(&sm.aempty[s], ((it / AS) & 1) ^ 1, kRbWaitNs)) { fail(); ok = false; break; }
+                            if (rank == 0) mbar_arrive_expect_tx(&sm.afull[s], (PAIR ? 2u : 1u) * 2 * kRbBox);
+                            if constexpr (PAIR)
+                                tma_load_2d_pair(sm.dx.a[s], &tm_dl, leader_bar(&sm.afull[s]), kb * 64, tile * kTok + static_cast<int>(rank) * 128);
+                            else
+                                tma_load_2d(sm.dx.a[s], &tm_dl, &sm.afull[s], kb * 64, tile * kTok);
                         }
                     }
-                    if constexpr (PAIR) umma_commit_pair(&sm.empty[s], 0x3); else umma_commit(&sm.empty[s]);
+                } else if (warp == 1 && lane == 0 && rank == 0) {
+                    uint32_t it = 0, ti = 0, panels = 0;
+                    int have = -1;
+                    const uint32_t idesc = f16_idesc(kTok, 256, false, false, true);
+                    bool ok = !sm.abort_flag;
+                    for (int u = x0; ok && u < x1 && !sm.abort_flag; ++u, ++ti) {
+                        const int panel = u / ttiles;
+                        if (panel != have) {
+                            have = panel;
+                            if (!mbar_wait(&sm.wfull, panels & 1, kRbWaitNs)) { fail(); break; }
+                            ++panels;
+                        }
+                        const uint32_t buf = ti & 1, d = tmem + buf * 256;
+                        if (!mbar_wait(&sm.tempty[0][buf], ((ti >> 1) & 1) ^ 1, kRbWaitNs)) { fail(); break; }
+                        tc_fence_after();
+                        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                            const int s = it % AS;
+                            if (!mbar_wait(&sm.afull[s], (it / AS) & 1, kRbWaitNs)) { fail(); ok = false; break; }
+                            tc_fence_after();
+                            const uint64_t da = sw128_kmajor_desc(smem_u32(sm.dx.a[s])), db = sw128_mnmajor_desc(smem_u32(sm.dx.w[kb]), kRbBox);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {           // 16 experts: 32 bytes on in a row, 2048 in the panel
+                                if constexpr (PAIR) umma_f16_pair(d, da + kk * 2, db + kk * 128, idesc, kb + kk > 0);
+                                else umma_f16(d, da + kk * 2, db + kk * 128, idesc, kb + kk > 0);
+                            }
+                            if constexpr (PAIR) umma_commit_pair(&sm.aempty[s], 0x3); else umma_commit(&sm.aempty[s]);
+                        }
+                        if (ok) {
+                            if constexpr (PAIR) umma_commit_pair(&sm.tfull[0][buf], 0x3); else umma_commit(&sm.tfull[0][buf]);
+                            if (u + 1 < x1 && (u + 1) / ttiles != panel) {
+                                if constexpr (PAIR) umma_commit_pair(&sm.wempty, 0x3); else umma_commit(&sm.wempty);
+                            }
+                        }
+                    }
                 }
-                if (ok) { if constexpr (PAIR) umma_commit_pair(&sm.tfull[buf], 0x3); else umma_commit(&sm.tfull[buf]); }
+            } else {
+                if (warp == 0 && lane == 0) {
+                    uint32_t it = 0;
+                    bool ok = !sm.abort_flag;
+                    const uint32_t bytes = (PAIR ? 2u : 1u) * stage_bytes;
+                    for (int u = u0; ok && u < u1; ++u) {
+                        const int tile = u / chunks, t0 = (u - tile * chunks) * kRbChunk;
+                        const int h0 = tile / g.etiles * kRows + static_cast<int>(rank) * 128;
+                        const int e0 = tile % g.etiles * kCols + static_cast<int>(rank) * 128;
+                        for (int t = t0; t < min(t0 + kRbChunk, g.T); t += 64, ++it) {
+                            const uint32_t s = it % depth;
+                            if (!mbar_wait(&sm.empty[s], ((it / depth) & 1) ^ 1, kRbWaitNs)) { fail(); ok = false; break; }
+                            if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], bytes);
+                            if constexpr (PAIR) {
+                                const uint32_t fb = leader_bar(&sm.full[s]);
+                                for (int i = 0; i < 2; ++i) tma_load_3d_pair(stage_x(s) + i * kRbBox, &tm_x, fb, h0 + 64 * i, t, 0);
+                                for (int p = 0; p < 3; ++p)
+                                    for (int i = 0; i < 2; ++i) tma_load_3d_pair(stage_d(s, p) + i * kRbBox, &tm_d, fb, e0 + 64 * i, t, p);
+                            } else {
+                                for (int i = 0; i < 2; ++i) tma_load_3d(stage_x(s) + i * kRbBox, &tm_x, &sm.full[s], h0 + 64 * i, t, 0);
+                                for (int p = 0; p < 3; ++p)
+                                    for (int i = 0; i < ebox; ++i) tma_load_3d(stage_d(s, p) + i * kRbBox, &tm_d, &sm.full[s], e0 + 64 * i, t, p);
+                            }
+                        }
+                    }
+                } else if (warp == 1 && lane == 0 && rank == 0) {
+                    uint32_t it = 0, ci = 0;
+                    bool ok = !sm.abort_flag;
+                    const uint32_t idesc = f16_idesc(kRows, PAIR ? 256 : (g.E + 15) / 16 * 16, true, true, true);
+                    for (int u = u0; ok && u < u1 && !sm.abort_flag; ++u, ++ci) {
+                        const int t0 = u % chunks * kRbChunk;
+                        const uint32_t buf = ci & 1, d = tmem + buf * 256;
+                        if (!mbar_wait(&sm.tempty[1][buf], ((ci >> 1) & 1) ^ 1, kRbWaitNs)) { fail(); break; }
+                        tc_fence_after();
+                        for (int t = t0; t < min(t0 + kRbChunk, g.T); t += 64, ++it) {
+                            const uint32_t s = it % depth;
+                            if (!mbar_wait(&sm.full[s], (it / depth) & 1, kRbWaitNs)) { fail(); ok = false; break; }
+                            tc_fence_after();
+                            // the descriptors' low bits hold address / 16: a slice of 16 tokens is 2048 bytes on. The three
+                            // parts of a slice share x, which the tensor core then reads once
+                            const uint64_t da = sw128_mnmajor_desc(smem_u32(stage_x(s)), kRbBox);
+                            const uint64_t db = sw128_mnmajor_desc(smem_u32(stage_d(s, 0)), kRbBox);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk) {
+                                const uint64_t a = da + kk * 128, b = db + kk * 128;
+                                umma_f16_keep<PAIR, KeepA::kFill>(d, a, b, idesc, kk > 0 || t > t0);
+                                umma_f16_keep<PAIR, KeepA::kUse>(d, a, b + part_step, idesc, 1);
+                                umma_f16_keep<PAIR, KeepA::kLast>(d, a, b + 2 * part_step, idesc, 1);
+                            }
+                            if constexpr (PAIR) umma_commit_pair(&sm.empty[s], 0x3); else umma_commit(&sm.empty[s]);
+                        }
+                        if (ok) { if constexpr (PAIR) umma_commit_pair(&sm.tfull[1][buf], 0x3); else umma_commit(&sm.tfull[1][buf]); }
+                    }
+                }
             }
+            turn_over();
         }
     } else {
         setmaxnreg_inc<kDwRegsHigh>();
-        // promotion: warp = lane quadrant q x half of the experts' columns
-        constexpr int kMine = kCols / 2;
-        const int q = warp & 3, half = (warp - 4) >> 2;
-        const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&sm.tempty[0]), 0) : 0u;
-        float acc[kMine];
-        uint32_t ci = 0;
-        for (int64_t u = u0; u < u1; ++u, ++ci) {
-            if (sm.abort_flag) break;
-            const int tile = static_cast<int>(u / chunks);
-            const bool begin = u == u0 || u % chunks == 0, end = u + 1 == u1 || (u + 1) % chunks == 0;
-            if (begin) {
+        for (int turn = 0; turn < 2; ++turn) {
+            if (turn == dx_turn) {
+                const int ew = warp - 4, q = warp & 3, half = ew >> 2;
+                // the warp's 32 rows x 128 columns of a unit as two boxes of 64 columns; box j goes through buffer
+                // j % NB: dx0 comes in one box ahead, dx leaves from the same place
+                const uint32_t boxes = static_cast<uint32_t>(2 * (x1 - x0));
+                auto place = [&](uint32_t j, int& row0, int& col0) {
+                    const int u = x0 + static_cast<int>(j >> 1);
+                    const int panel = u / ttiles, tile = u - panel * ttiles;
+                    row0 = tile * kTok + static_cast<int>(rank) * 128 + q * 32;
+                    col0 = panel * 256 + half * 128 + 64 * static_cast<int>(j & 1);
+                };
+                auto fetch = [&](uint32_t j) {         // lane 0
+                    int row0, col0;
+                    place(j, row0, col0);
+                    uint64_t* bar = &sm.eload[ew][j % NB];
+                    mbar_arrive_expect_tx(bar, 4096);
+                    tma_load_2d(sm.dx.stage[ew][j % NB], &tm_in, bar, col0, row0);
+                };
+                if (g.has_base && lane == 0 && boxes > 0 && !sm.abort_flag) fetch(0);
+                float sc = 0.0f;
+                for (uint32_t j = 0; j < boxes; ++j) {
+                    if (sm.abort_flag) break;
+                    const uint32_t ti = j >> 1, buf = ti & 1, n = j % NB;
+                    int row0, col0;
+                    place(j, row0, col0);
+                    if (!(j & 1)) sc = row0 + lane < g.T ? g.tscale[row0 + lane] : 0.0f;
+                    if (lane == 0) {
+                        bulk_wait_read<NB - 2>();      // box j + 1 - NB has left the buffer that box j + 1 goes to
+                        if (g.has_base && j + 1 < boxes) fetch(j + 1);
+                    }
+                    __syncwarp();
+                    if (!(j & 1)) {
+                        if (!mbar_wait(&sm.tfull[0][buf], (ti >> 1) & 1, kRbWaitNs)) { fail(); break; }
+                        tc_fence_after();
+                    }
+                    if (g.has_base && !mbar_wait(&sm.eload[ew][n], (j / NB) & 1, kRbWaitNs)) { fail(); break; }
+                    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * 128 + 64 * (j & 1);
 #pragma unroll
-                for (int i = 0; i < kMine; ++i) acc[i] = 0.0f;
-            }
-            const uint32_t buf = ci & 1;
-            if (!mbar_wait(&sm.tfull[buf], (ci >> 1) & 1, kRbWaitNs)) { fail(); break; }
-            tc_fence_after();
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * kMine;
+                    for (int i = 0; i < 2; ++i) {      // 32 columns at a time
+                        float v[32];
+                        tmem_ld32(taddr + 32 * i, v);
+                        // 16-byte piece p of row `lane` sits at p ^ (lane & 7)
+                        const uint32_t st = smem_u32(sm.dx.stage[ew][n]) + lane * 128;
+                        auto at = [&](int p) { return st + (((i * 4 + p) ^ (lane & 7)) << 4); };
+                        uint32_t b[4][4] = {};
+                        if (g.has_base) {
 #pragma unroll
-            for (int c = 0; c < kMine / 32; ++c) {
-                float v[32];
-                tmem_ld32(taddr + 32 * c, v);
-                tmem_ld_wait();
+                            for (int p = 0; p < 4; ++p)
+                                asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(b[p][0]), "=r"(b[p][1]), "=r"(b[p][2]), "=r"(b[p][3]) : "r"(at(p)) : "memory");
+                        }
+                        tmem_ld_wait();
+                        if (i == 1 && (j & 1)) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) release(&sm.tempty[0][buf]);
+                        }
 #pragma unroll
-                for (int i = 0; i < 32; ++i) acc[32 * c + i] += v[i];
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (PAIR && rank) mbar_arrive_cluster(tempty0 + buf * static_cast<uint32_t>(sizeof(uint64_t)));
-                else mbar_arrive(&sm.tempty[buf]);
-            }
-            if (end) {
-                // partial tile [kCols][kRows]: a warp's store is 32 consecutive rows of one expert
-                float* dst = part + (static_cast<int64_t>(tile) + grp) * kCols * kRows + rank * 128 + q * 32 + lane;
-                const int ecount = E - tile % etiles * kCols;
+                        for (int p = 0; p < 4; ++p) {
+                            uint32_t o[4];
 #pragma unroll
-                for (int i = 0; i < kMine; ++i)
-                    if (half * kMine + i < ecount) dst[(half * kMine + i) * kRows] = acc[i];
+                            for (int k = 0; k < 4; ++k) {
+                                const float2 y = __ffma2_rn(make_float2(v[p * 8 + 2 * k], v[p * 8 + 2 * k + 1]), make_float2(sc, sc),
+                                                            make_float2(__uint_as_float(b[p][k] << 16), __uint_as_float(b[p][k] & 0xffff0000u)));
+                                const __nv_bfloat162 r = __floats2bfloat162_rn(y.x, y.y);
+                                o[k] = *reinterpret_cast<const uint32_t*>(&r);
+                            }
+                            st_shared_v4(at(p), o[0], o[1], o[2], o[3]);
+                        }
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (row0 < g.T && col0 < g.H) tma_store_2d(&tm_out, sm.dx.stage[ew][n], col0, row0);
+                        bulk_commit();
+                    }
+                }
+                if (lane == 0) bulk_wait_read_all();
+            } else {
+                // promotion: warp = lane quadrant q x half of the experts' columns
+                constexpr int kMine = kCols / 2;
+                const int q = warp & 3, half = (warp - 4) >> 2;
+                float acc[kMine];
+                uint32_t ci = 0;
+                for (int u = u0; u < u1; ++u, ++ci) {
+                    if (sm.abort_flag) break;
+                    const int tile = u / chunks;
+                    const bool begin = u == u0 || u % chunks == 0, end = u + 1 == u1 || (u + 1) % chunks == 0;
+                    if (begin) {
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i) acc[i] = 0.0f;
+                    }
+                    const uint32_t buf = ci & 1;
+                    if (!mbar_wait(&sm.tfull[1][buf], (ci >> 1) & 1, kRbWaitNs)) { fail(); break; }
+                    tc_fence_after();
+                    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * kMine;
+#pragma unroll
+                    for (int c = 0; c < kMine / 32; ++c) {
+                        float v[32];
+                        tmem_ld32(taddr + 32 * c, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) acc[32 * c + i] += v[i];
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) release(&sm.tempty[1][buf]);
+                    if (end) {
+                        // partial tile [kCols][kRows]: a warp's store is 32 consecutive rows of one expert
+                        float* dst = g.part + (static_cast<int64_t>(tile) + grp) * kCols * kRows + rank * 128 + q * 32 + lane;
+                        const int ecount = g.E - tile % g.etiles * kCols;
+#pragma unroll
+                        for (int i = 0; i < kMine; ++i)
+                            if (half * kMine + i < ecount) dst[(half * kMine + i) * kRows] = acc[i];
+                    }
+                }
             }
+            turn_over();
         }
+        if (lane == 0) bulk_wait_all();               // dx's stores have completed
     }
+    __syncwarp();
     tc_fence_before();
     if constexpr (PAIR) cluster_sync(); else __syncthreads();
     if (sm.abort_flag) {
         const uint64_t t0 = globaltimer_ns();
-        while (globaltimer_ns() - t0 < 200000) __nanosleep(1000);
+        while (globaltimer_ns() - t0 < 200000) __nanosleep(1000);   // copies and MMAs in flight land
     }
     if constexpr (PAIR) cluster_sync(); else __syncthreads();
     if (warp == 1) {
@@ -464,40 +554,175 @@ router_dw_kernel(const __grid_constant__ CUtensorMap tm_x, const __grid_constant
     }
 }
 
-// ---------------------------------------------------------------- 4. sums of the partial tiles, db
+// ---------------------------------------------------------------- 3. sums of the partial tiles, db
+// The groups that touched each tile: first[t] .. last[t] (at most 128 tiles, 160 groups).
+struct TileGroups {
+    uint8_t first[128], last[128];
+};
+
+// Block (x, e): 1024 columns of expert e, four a thread; the first 32 threads of column block 0 also db[e].
 __global__ void __launch_bounds__(256)
-router_finish_kernel(const float* __restrict__ part, const float* __restrict__ dbpart, int T, int H, int E, int rows,
-                     int cols, int etiles, int chunks, int64_t U, int G, int db_blocks, const float* dWg0,
+router_finish_kernel(const float* __restrict__ part, const float* __restrict__ dbpart, const __grid_constant__ TileGroups tg,
+                     int H, int E, int rows, int cols, int etiles, int summed, int db_blocks, const float* dWg0,
                      const float* db0, float* dWg, float* db) {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t n = static_cast<int64_t>(E) * (H / 4);
-    if (i < n) {
-        const int e = static_cast<int>(i / (H / 4)), h = static_cast<int>(i % (H / 4)) * 4;
+    const int e = blockIdx.y, h = (blockIdx.x * 256 + threadIdx.x) * 4;
+    dependents_may_launch();
+    wait_for_producers();
+    if (h < H) {
+        const int64_t at = static_cast<int64_t>(e) * H + h;
         float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (dWg0) s = *reinterpret_cast<const float4*>(dWg0 + static_cast<int64_t>(e) * H + h);
-        if (U > 0) {
-            const int tile = h / rows * etiles + e / cols;
-            const int g0 = group_of(U, G, static_cast<int64_t>(tile) * chunks);
-            const int g1 = group_of(U, G, static_cast<int64_t>(tile + 1) * chunks - 1);
+        if (dWg0) s = *reinterpret_cast<const float4*>(dWg0 + at);
+        if (summed) {
+            const int tile = h / rows * etiles + e / cols, g0 = tg.first[tile], n = tg.last[tile] - g0 + 1;
+            const int64_t step = static_cast<int64_t>(cols) * rows;
+            const float* p = part + (tile + g0) * step + static_cast<int64_t>(e % cols) * rows + h % rows;
             float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int g = g0; g <= g1; ++g) {
-                const float4 p = *reinterpret_cast<const float4*>(
-                    part + ((static_cast<int64_t>(tile) + g) * cols + e % cols) * rows + h % rows);
-                a.x += p.x; a.y += p.y; a.z += p.z; a.w += p.w;
+            for (int g = 0; g < n; g += 4) {
+                float4 v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = g + i < n ? *reinterpret_cast<const float4*>(p + (g + i) * step) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) { a.x += v[i].x; a.y += v[i].y; a.z += v[i].z; a.w += v[i].w; }
             }
             s.x += a.x; s.y += a.y; s.z += a.z; s.w += a.w;
         }
-        *reinterpret_cast<float4*>(dWg + static_cast<int64_t>(e) * H + h) = s;
+        *reinterpret_cast<float4*>(dWg + at) = s;
     }
-    // db: a warp an expert, the first warps of the grid
-    const int64_t e = i >> 5;
-    if (e < E) {
-        const int lane = threadIdx.x & 31;
+    if (blockIdx.x == 0 && threadIdx.x < 32) {
         double s = 0.0;
-        for (int b = lane; b < db_blocks; b += 32) s += dbpart[static_cast<int64_t>(b) * E + e];
+#pragma unroll 4
+        for (int b = threadIdx.x; b < db_blocks; b += 32) s += dbpart[static_cast<int64_t>(b) * E + e];
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == 0) db[e] = static_cast<float>(s + (db0 ? db0[e] : 0.0));
+        if (threadIdx.x == 0) db[e] = static_cast<float>(s + (db0 ? db0[e] : 0.0));
+    }
+}
+
+// ---------------------------------------------------------------- few tokens: both products on the CUDA cores
+// One launch instead of four, fp32 throughout. The first dx_blocks blocks: 16 tokens x 256 columns of dx, a thread 4
+// tokens x 4 columns, dl transposed in shared memory. The others: 64 columns x 16 experts of dWg over all tokens, a
+// thread 4 columns x 16 experts of every 16th token, the 16 slices added in order; those of column tile 0 also db.
+constexpr int kDirTok = 16, kDirCols = 256;              // dx tile
+constexpr int kDirH = 64, kDirE = 16, kDirChunk = 128;   // dWg tile, tokens of dl staged at a time
+
+template <bool BASE>
+__global__ void __launch_bounds__(256)
+router_direct_kernel(const uint16_t* __restrict__ x, const float* __restrict__ Wg, const float* __restrict__ dl, int T, int H,
+                     int E, int dx_blocks, const uint16_t* dx0, const float* dWg0, const float* db0, uint16_t* dx,
+                     float* dWg, float* db) {
+    extern __shared__ float sm_f[];
+    const int tid = threadIdx.x;
+    dependents_may_launch();
+    wait_for_producers();
+    if (static_cast<int>(blockIdx.x) < dx_blocks) {
+        const int ct = (H + kDirCols - 1) / kDirCols;
+        const int t0 = blockIdx.x / ct * kDirTok, h = blockIdx.x % ct * kDirCols + (tid & 63) * 4, tg = tid >> 6;
+        float* sd = sm_f;                                 // [E][16]
+        for (int i = tid; i < E * kDirTok; i += 256) {
+            const int t = i / E, e = i - t * E;
+            sd[e * kDirTok + t] = t0 + t < T ? dl[static_cast<int64_t>(t0 + t) * E + e] : 0.0f;
+        }
+        __syncthreads();
+        if (h >= H) return;
+        float acc[4][4] = {};
+#pragma unroll 8
+        for (int e = 0; e < E; ++e) {
+            const float4 w = __ldg(reinterpret_cast<const float4*>(Wg + static_cast<int64_t>(e) * H + h));
+            const float4 d = *reinterpret_cast<const float4*>(sd + e * kDirTok + tg * 4);
+            const float dd[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i][0] = fmaf(dd[i], w.x, acc[i][0]);
+                acc[i][1] = fmaf(dd[i], w.y, acc[i][1]);
+                acc[i][2] = fmaf(dd[i], w.z, acc[i][2]);
+                acc[i][3] = fmaf(dd[i], w.w, acc[i][3]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = t0 + tg * 4 + i;
+            if (t >= T) break;
+            const int64_t at = static_cast<int64_t>(t) * H + h;
+            if (BASE) {
+                const uint2 b = *reinterpret_cast<const uint2*>(dx0 + at);
+                acc[i][0] += __uint_as_float(b.x << 16);
+                acc[i][1] += __uint_as_float(b.x & 0xffff0000u);
+                acc[i][2] += __uint_as_float(b.y << 16);
+                acc[i][3] += __uint_as_float(b.y & 0xffff0000u);
+            }
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[i][0], acc[i][1]), hi = __floats2bfloat162_rn(acc[i][2], acc[i][3]);
+            *reinterpret_cast<uint2*>(dx + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+        }
+        return;
+    }
+    const int b = blockIdx.x - dx_blocks, ht = H / kDirH;
+    const int h = b % ht * kDirH + (tid & 15) * 4, e0 = b / ht * kDirE, slice = tid >> 4;
+    float* sd = sm_f;                                     // [128][16], then the slices' sums [16][16][64]
+    float acc[kDirE][4] = {};
+    float dsum = 0.0f;
+    for (int c0 = 0; c0 < T; c0 += kDirChunk) {
+        uint2 xv[kDirChunk / 16];
+#pragma unroll
+        for (int i = 0; i < kDirChunk / 16; ++i) {
+            const int t = c0 + slice + 16 * i;
+            xv[i] = t < T ? *reinterpret_cast<const uint2*>(x + static_cast<int64_t>(t) * H + h) : make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int i = 0; i < kDirChunk * kDirE / 256; ++i) {
+            const int j = tid + 256 * i, t = c0 + j / kDirE, e = e0 + j % kDirE;
+            sd[j] = t < T && e < E ? dl[static_cast<int64_t>(t) * E + e] : 0.0f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kDirChunk / 16; ++i) {
+            const float xx[4] = {__uint_as_float(xv[i].x << 16), __uint_as_float(xv[i].x & 0xffff0000u),
+                                 __uint_as_float(xv[i].y << 16), __uint_as_float(xv[i].y & 0xffff0000u)};
+            const float* d = sd + (slice + 16 * i) * kDirE;
+#pragma unroll
+            for (int e = 0; e < kDirE; e += 4) {
+                const float4 f = *reinterpret_cast<const float4*>(d + e);
+                const float ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) acc[e + j][c] = fmaf(ff[j], xx[c], acc[e + j][c]);
+            }
+            dsum += d[tid & 15];
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int e = 0; e < kDirE; ++e)
+        *reinterpret_cast<float4*>(sm_f + (slice * kDirE + e) * kDirH + (tid & 15) * 4) = make_float4(acc[e][0], acc[e][1], acc[e][2], acc[e][3]);
+    __syncthreads();
+    {
+        // the slices of (expert tid / 16, four columns)
+        const int e = tid >> 4, col = (tid & 15) * 4;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(sm_f + (i * kDirE + e) * kDirH + col);
+            s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+        }
+        if (e0 + e < E) {
+            const int64_t at = static_cast<int64_t>(e0 + e) * H + h;
+            if (dWg0) {
+                const float4 v = *reinterpret_cast<const float4*>(dWg0 + at);
+                s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            }
+            *reinterpret_cast<float4*>(dWg + at) = s;
+        }
+    }
+    if (b % ht == 0) {
+        __syncthreads();
+        sm_f[tid] = dsum;                                 // [slice][expert]
+        __syncthreads();
+        if (tid < kDirE && e0 + tid < E) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s += sm_f[i * kDirE + tid];
+            db[e0 + tid] = s + (db0 ? db0[e0 + tid] : 0.0f);
+        }
     }
 }
 
@@ -505,12 +730,10 @@ router_finish_kernel(const float* __restrict__ part, const float* __restrict__ d
 struct RbPlan {
     bool pair;
     int rows, cols, htiles, etiles, chunks;
-    int64_t U;
+    int U;
     int most_groups;      // partial tiles: htiles * etiles + groups
 };
 
-// Experts above 128 run as CTA pairs: their operand of dl is then read once for 256 columns of x, and 64 KB a
-// stage instead of 112 KB cross from L2 for the same MMAs.
 RbPlan plan_of(int T, int H, int E) {
     RbPlan p;
     p.pair = E > 128;
@@ -519,7 +742,7 @@ RbPlan plan_of(int T, int H, int E) {
     p.htiles = (H + p.rows - 1) / p.rows;
     p.etiles = (E + p.cols - 1) / p.cols;
     p.chunks = (T + kRbChunk - 1) / kRbChunk;
-    p.U = static_cast<int64_t>(p.htiles) * p.etiles * p.chunks;
+    p.U = p.htiles * p.etiles * p.chunks;      // below 2^31: T is below 2^24
     p.most_groups = p.pair ? 80 : 160;
     return p;
 }
@@ -571,44 +794,48 @@ bool make_map16(CUtensorMap* m, const void* base, bool bf16, int64_t cols, int64
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int PN, bool BASE>
-cudaError_t launch_dx(const CUtensorMap& dl, const CUtensorMap& w, const CUtensorMap& in, const CUtensorMap& out,
-                      const float* tscale, int T, int H, int E, int* status, int num_sms, cudaStream_t s) {
-    const size_t smem = sizeof(SmemX<PN>) + 1024;
-    cudaError_t err = cudaFuncSetAttribute(router_dx_kernel<PN, BASE>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+// Up to 512 tokens and 2^25 products of either kind the one launch wins. Measured on a B200 (us, replayed; direct /
+// tensor cores): 256 x 512 x 8 4.8 / 14.7, 256 x 2048 x 64 (2^25) 7.6 / 15.9, 512 x 4096 x 64 (2^27) 24.6 / 17.5,
+// 4096 x 512 x 16 (2^25) 49 / 22.
+bool use_direct(int T, int H, int E) { return T <= 512 && static_cast<int64_t>(T) * H * E <= (1ll << 25); }
+
+cudaError_t launch_direct(const uint16_t* x, const float* Wg, const float* dl, int T, int H, int E, const uint16_t* dx0,
+                          const float* dWg0, const float* db0, uint16_t* dx, float* dWg, float* db, cudaStream_t s) {
+    auto kern = dx0 ? router_direct_kernel<true> : router_direct_kernel<false>;
+    const int smem = sizeof(float) * std::max(E * kDirTok, 16 * kDirE * kDirH);
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
-    const int panels = (H + PN - 1) / PN, tiles = (T + 127) / 128;
-    const int64_t grid = std::min<int64_t>(std::max(num_sms, panels), static_cast<int64_t>(panels) * tiles);
-    router_dx_kernel<PN, BASE><<<static_cast<int>(grid), kRbThreads, smem, s>>>(dl, w, in, out, tscale, T, H, E, panels, status);
-    return cudaGetLastError();
+    const int dx_blocks = (T + kDirTok - 1) / kDirTok * ((H + kDirCols - 1) / kDirCols);
+    const int dw_blocks = H / kDirH * ((E + kDirE - 1) / kDirE);
+    return launch_dependent(kern, dim3(dx_blocks + dw_blocks), dim3(256), smem, s, x, Wg, dl, T, H, E, dx_blocks, dx0, dWg0, db0,
+                            dx, dWg, db);
 }
 
-template <bool PAIR>
-cudaError_t launch_dw(const CUtensorMap& x, const CUtensorMap& d, int T, int H, int E, const RbPlan& p, float* part,
-                      int* status, int num_sms, cudaStream_t s, int* groups) {
-    auto kern = router_dw_kernel<PAIR>;
-    const size_t smem = sizeof(SmemW) + 1024;
+template <bool PAIR, int KB, int AS, int NB>
+cudaError_t launch_products(const CUtensorMap (&m)[6], const RouterArgs& g, int groups, cudaStream_t s) {
+    auto kern = router_products_kernel<PAIR, KB, AS, NB>;
+    const size_t smem = sizeof(SmemP<PAIR, KB, AS, NB>) + 1024;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
+    // a setmaxnreg.inc can only draw on what the block was launched with: refuse a build with less
     cudaFuncAttributes fa;
     if ((err = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return err;
     if (fa.numRegs * kRbThreads < kDwRegsSplit) return cudaErrorInvalidConfiguration;
-    int G = std::min(PAIR ? num_sms / 2 : num_sms, p.most_groups);
-    G = static_cast<int>(std::min<int64_t>(G, p.U));
-    *groups = G;
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3(PAIR ? 2 * G : G);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(PAIR ? 2 * groups : groups);
     cfg.blockDim = dim3(kRbThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = PAIR ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, kern, x, d, T, H, E, p.etiles, p.U, G, part, status);
+    cfg.numAttrs = PAIR ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], g);
 }
 
 moe_status_t check_router(int T, int H, int E) {
@@ -649,32 +876,53 @@ moe_status_t moe_router_backward(int T, int H, int E, const void* x, const float
     const RbPlan p = plan_of(T, H, E);
     const int ld = (E + 7) / 8 * 8, db_blocks = (T + kPrepTokens - 1) / kPrepTokens;
     auto ok = [](cudaError_t e) { return e == cudaSuccess; };
-    int G = 1;
+    if (T > 0 && use_direct(T, H, E))
+        return ok(launch_direct(static_cast<const uint16_t*>(x), Wg, dlogits, T, H, E, static_cast<const uint16_t*>(dx0), dWg0, db0,
+                                static_cast<uint16_t*>(dx), dWg, db, s))
+                   ? MOE_OK
+                   : MOE_ERR_CUDA;
+    TileGroups tg = {};
     if (T > 0) {
-        router_prep_w_kernel<<<E, 256, 0, s>>>(Wg, H, w.wh, w.wscale);
-        router_prep_dl_kernel<<<db_blocks, 256, 0, s>>>(dlogits, w.wscale, T, E, ld, w.dlh, w.tscale, w.parts, w.dbpart);
-        if (!ok(cudaGetLastError())) return MOE_ERR_CUDA;
-        CUtensorMap m_dl, m_w, m_in, m_out, m_x, m_d;
-        if (!make_map16(&m_dl, w.dlh, false, E, T, 1, ld, 128, 2) || !make_map16(&m_w, w.wh, false, H, E, 1, H, 64, 2) ||
-            !make_map16(&m_in, dx0 ? dx0 : dx, true, H, T, 1, H, 32, 2) || !make_map16(&m_out, dx, true, H, T, 1, H, 32, 2) ||
-            !make_map16(&m_x, x, true, H, T, 1, H, 64, 3) || !make_map16(&m_d, w.parts, true, E, T, 3, ld, 64, 3))
+        if (!ok(launch_dependent(router_prep_w_kernel, dim3(E), dim3(256), 0, s, Wg, H, w.wh, w.wscale))) return MOE_ERR_CUDA;
+        const bool vec = E % 4 == 0;
+        auto prep = E <= 128   ? (vec ? router_prep_dl_kernel<1, true> : router_prep_dl_kernel<1, false>)
+                    : E <= 256 ? (vec ? router_prep_dl_kernel<2, true> : router_prep_dl_kernel<2, false>)
+                               : (vec ? router_prep_dl_kernel<4, true> : router_prep_dl_kernel<4, false>);
+        if (!ok(launch_dependent(prep, dim3(db_blocks), dim3(256), 0, s, dlogits, w.wscale, T, E, ld, w.dlh, w.tscale, w.parts, w.dbpart)))
             return MOE_ERR_CUDA;
-        cudaError_t err;
-        if (E <= 256)
-            err = dx0 ? launch_dx<256, true>(m_dl, m_w, m_in, m_out, w.tscale, T, H, E, status, num_sms, s)
-                      : launch_dx<256, false>(m_dl, m_w, m_in, m_out, w.tscale, T, H, E, status, num_sms, s);
-        else
-            err = dx0 ? launch_dx<128, true>(m_dl, m_w, m_in, m_out, w.tscale, T, H, E, status, num_sms, s)
-                      : launch_dx<128, false>(m_dl, m_w, m_in, m_out, w.tscale, T, H, E, status, num_sms, s);
-        if (!ok(err)) return MOE_ERR_CUDA;
-        err = p.pair ? launch_dw<true>(m_x, m_d, T, H, E, p, w.part, status, num_sms, s, &G)
-                     : launch_dw<false>(m_x, m_d, T, H, E, p, w.part, status, num_sms, s, &G);
+        CUtensorMap m[6];
+        if (!make_map16(&m[0], w.dlh, false, E, T, 1, ld, 128, 2) || !make_map16(&m[1], w.wh, false, H, E, 1, H, 64, 2) ||
+            !make_map16(&m[2], dx0 ? dx0 : dx, true, H, T, 1, H, 32, 2) || !make_map16(&m[3], dx, true, H, T, 1, H, 32, 2) ||
+            !make_map16(&m[4], x, true, H, T, 1, H, 64, 3) || !make_map16(&m[5], w.parts, true, E, T, 3, ld, 64, 3))
+            return MOE_ERR_CUDA;
+        RouterArgs g;
+        g.T = T;
+        g.H = H;
+        g.E = E;
+        g.has_base = dx0 != nullptr;
+        const int tok = p.pair ? 256 : 128, groups = std::min(p.pair ? num_sms / 2 : num_sms, p.most_groups);
+        g.Ux = (H + 255) / 256 * ((T + tok - 1) / tok);
+        g.Uw = p.U;
+        g.Gx = std::min(groups, g.Ux);
+        g.Gw = std::min(groups, g.Uw);
+        for (int t = 0; t < p.htiles * p.etiles; ++t) {
+            tg.first[t] = static_cast<uint8_t>(group_of(g.Uw, g.Gw, t * p.chunks));
+            tg.last[t] = static_cast<uint8_t>(group_of(g.Uw, g.Gw, (t + 1) * p.chunks - 1));
+        }
+        g.etiles = p.etiles;
+        g.tscale = w.tscale;
+        g.part = w.part;
+        g.status = status;
+        const int used = std::max(g.Gx, g.Gw);
+        const cudaError_t err = !p.pair    ? launch_products<false, 2, 4, 3>(m, g, used, s)
+                                : E <= 256 ? launch_products<true, 4, 4, 3>(m, g, used, s)
+                                           : launch_products<true, 8, 2, 2>(m, g, used, s);
         if (!ok(err)) return MOE_ERR_CUDA;
     }
-    const int64_t work = std::max<int64_t>(static_cast<int64_t>(E) * (H / 4), 32ll * E);
-    router_finish_kernel<<<static_cast<int>((work + 255) / 256), 256, 0, s>>>(
-        w.part, w.dbpart, T, H, E, p.rows, p.cols, p.etiles, p.chunks, p.U, G, db_blocks, dWg0, db0, dWg, db);
-    return ok(cudaGetLastError()) ? MOE_OK : MOE_ERR_CUDA;
+    return ok(launch_dependent(router_finish_kernel, dim3((H + 1023) / 1024, E), dim3(256), 0, s, w.part, w.dbpart, tg, H, E, p.rows,
+                               p.cols, p.etiles, T > 0 ? 1 : 0, db_blocks, dWg0, db0, dWg, db))
+               ? MOE_OK
+               : MOE_ERR_CUDA;
 }
 
 }  // extern "C"
