@@ -36,10 +36,16 @@ constexpr int kOK = 64;                      // K values a stage holds: 128 byte
 constexpr int kOStages = 5;
 constexpr int kOBox = 64 * kOK * 2;          // one 64 x 64 box of an operand: 8 KB
 constexpr int kOOper = 2 * kOBox;            // a CTA's 128 rows of an operand
+// "What a tile needs is there", from the producer to the epilogue warps, a barrier a tile in turn. While an epilogue
+// warp is at a tile the producer is at most 2 (accumulators) + kOStages (tiles of one K block in the ring) ahead, so a
+// barrier is not reused before it was waited for.
+constexpr int kOReady = 16;
+static_assert(kOReady > kOStages + 3, "a tile's barrier must outlast the tiles in flight");
 constexpr int kOThreads = 384;               // TMA, MMA, two idle warps, eight epilogue warps
 constexpr int kOEpi = 8;
 constexpr float kPScale = 64.0f;             // A and B are stored times this
 constexpr int kMaxSteps = 32;
+constexpr int kDoneStride = 32;              // matrices' counters lie 128 bytes apart: each is polled by many CTAs
 
 struct SmemO {
     uint8_t a[kOStages][kOOper];
@@ -51,6 +57,7 @@ struct SmemO {
     uint64_t tempty[2];
     uint64_t eload[kOEpi];
     uint64_t stored;
+    uint64_t ready[kOReady];
     uint32_t tmem_base;
     volatile int abort_flag;
 };
@@ -72,7 +79,7 @@ struct OrthoArgs {
     float out_scale;         // scale / the power of two X is stored with
     float gram_scale;        // 64 / that power squared
     uint16_t* O;             // the wave's first matrix
-    unsigned* done;          // [mats] finished tiles, counted by every CTA
+    unsigned* done;          // [mats][kDoneStride] finished tiles, counted by every CTA
     int* status;
 };
 
@@ -186,6 +193,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
         }
         for (int i = 0; i < kOEpi; ++i) mbar_init(&sm.eload[i], 1);
         mbar_init(&sm.stored, kOEpi);
+        for (int i = 0; i < kOReady; ++i) mbar_init(&sm.ready[i], 1);
         sm.abort_flag = 0;
         fence_mbar_init();
     }
@@ -205,9 +213,10 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
     };
     // Waits until matrix b's counter reaches `need`, then lets later TMA accesses see what was stored before it.
     auto wait_for = [&](int b, unsigned need) -> bool {
-        if (load_acquire_gpu(g.done + b) < need) {
+        const unsigned* done = g.done + b * kDoneStride;
+        if (load_acquire_gpu(done) < need) {
             const uint64_t t0 = globaltimer_ns();
-            while (load_acquire_gpu(g.done + b) < need) {
+            while (load_acquire_gpu(done) < need) {
                 if (sm.abort_flag || globaltimer_ns() - t0 > kOrthoWaitNs) return false;
                 __nanosleep(20);
             }
@@ -219,11 +228,12 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
     if (warp == 0) {
         // ---------------- producer: this CTA's 128 rows of the A operand and its half of the B operand
         if (lane == 0) {
-            uint32_t it = 0;
+            uint32_t it = 0, ti = 0;
             bool ok = true;
-            for (; ok && w.more(); w.next()) {
+            for (; ok && w.more(); w.next(), ++ti) {
                 const OrthoTile t = w.tile();
                 if (!wait_for(t.b, w.needs())) { fail(); break; }
+                mbar_arrive(&sm.ready[ti % kOReady]);                  // for the epilogue warps' loads of this tile
                 const int cur = t.step & 1;
                 // product 0: X X^T (X^T X); 1: A A; 2: B X (X B)
                 const CUtensorMap* ma = t.prod == 0 ? &maps.hi_op[cur] : t.prod == 1 ? &maps.p_op : sh.tall ? &maps.hi_op[cur] : &maps.q_op;
@@ -231,21 +241,22 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                 const bool a_mn = t.prod == 0 && sh.tall;
                 const bool b_mn = (t.prod == 0 && sh.tall) || (t.prod == 2 && !sh.tall);
                 const int K = t.prod == 0 ? sh.l : sh.s;
+                const bool same = t.prod != 2 && t.ti == t.tj;   // a diagonal tile: both operands are the same rows
                 const int ra = t.ti * kEdge + static_cast<int>(rank) * 128, rb = t.tj * kEdge + static_cast<int>(rank) * 128;
                 for (int k0 = 0; k0 < K; k0 += kOK, ++it) {
                     const int s = it % kOStages;
                     if (!mbar_wait(&sm.empty[s], ((it / kOStages) & 1) ^ 1, kOrthoWaitNs)) { fail(); ok = false; break; }
                     const uint32_t fb = PAIR ? mapa_shared(smem_u32(&sm.full[s]), 0) : 0u;
-                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], (PAIR ? 4 : 2) * kOOper);
+                    if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], (PAIR ? 2 : 1) * (same ? 1 : 2) * kOOper);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
                         const int ya = ra + 64 * i, yb = rb + 64 * i;
                         if constexpr (PAIR) {
                             tma_load_3d_pair(sm.a[s] + i * kOBox, ma, fb, a_mn ? ya : k0, a_mn ? k0 : ya, t.b);
-                            tma_load_3d_pair(sm.b[s] + i * kOBox, mb, fb, b_mn ? yb : k0, b_mn ? k0 : yb, t.b);
+                            if (!same) tma_load_3d_pair(sm.b[s] + i * kOBox, mb, fb, b_mn ? yb : k0, b_mn ? k0 : yb, t.b);
                         } else {
                             tma_load_3d(sm.a[s] + i * kOBox, ma, &sm.full[s], a_mn ? ya : k0, a_mn ? k0 : ya, t.b);
-                            tma_load_3d(sm.b[s] + i * kOBox, mb, &sm.full[s], b_mn ? yb : k0, b_mn ? k0 : yb, t.b);
+                            if (!same) tma_load_3d(sm.b[s] + i * kOBox, mb, &sm.full[s], b_mn ? yb : k0, b_mn ? k0 : yb, t.b);
                         }
                     }
                 }
@@ -273,7 +284,8 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                     // 16 K values on (the descriptors hold address / 16): 32 bytes in a K-major row, 16 rows of 128 bytes
                     // of an MN-major box
                     uint64_t da = a_mn ? sw128_mnmajor_desc(smem_u32(sm.a[s]), kOBox) : sw128_kmajor_desc(smem_u32(sm.a[s]));
-                    uint64_t db = b_mn ? sw128_mnmajor_desc(smem_u32(sm.b[s]), kOBox) : sw128_kmajor_desc(smem_u32(sm.b[s]));
+                    const uint32_t b0 = smem_u32(t.prod != 2 && t.ti == t.tj ? sm.a[s] : sm.b[s]);
+                    uint64_t db = b_mn ? sw128_mnmajor_desc(b0, kOBox) : sw128_kmajor_desc(b0);
 #pragma unroll
                     for (int kk = 0; kk < kOK / 16; ++kk, da += a_step, db += b_step) {
                         if constexpr (PAIR) umma_f16_pair(d, da, db, idesc, k0 + kk > 0);
@@ -310,7 +322,10 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                 if (lane == 0) {
                     bulk_wait_read_all();
                     if (t.prod != 0) {
-                        if (sub == 0) good = wait_for(t.b, w.needs());
+                        if (sub == 0) {
+                            good = mbar_wait(&sm.ready[ti % kOReady], (ti / kOReady) & 1, kOrthoWaitNs);
+                            fence_proxy_async();
+                        }
                         if (good) {
                             mbar_arrive_expect_tx(&sm.eload[ew], t.prod == 1 ? 4096 : 8192);
                             if (t.prod == 1) {
@@ -469,7 +484,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                     mbar_arrive(&sm.stored);
                     if (ew == 0) {
                         good = mbar_wait(&sm.stored, tiles & 1, kOrthoWaitNs);
-                        if (good) add_release_gpu(g.done + t.b, 1);
+                        if (good) add_release_gpu(g.done + t.b * kDoneStride, 1);
                     }
                 }
                 ++tiles;
@@ -561,7 +576,7 @@ ortho_norm_kernel(const void* __restrict__ G, int M, int N, int interleaved, dou
     const int64_t n = static_cast<int64_t>(M) * N;
     dependents_may_launch();
     wait_for_producers();
-    if (blockIdx.x == 0 && threadIdx.x == 0) done[m] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) done[m * kDoneStride] = 0;
     double s = 0.0;
     for (int64_t e = (static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x) * kNormVals; e < n;
          e += static_cast<int64_t>(gridDim.x) * kNormThreads * kNormVals) {
@@ -652,7 +667,7 @@ OrthoWs carve_ortho(int wave, int M, int N, void* base) {
     w.p = reinterpret_cast<uint16_t*>(take(2 * wave * s * lds));
     w.q = reinterpret_cast<uint16_t*>(take(2 * wave * s * lds));
     w.part = reinterpret_cast<double*>(take(8ull * wave * kNormBlocks));
-    w.done = reinterpret_cast<unsigned*>(take(4ull * wave));
+    w.done = reinterpret_cast<unsigned*>(take(4ull * wave * kDoneStride));
     w.total = off;
     return w;
 }
