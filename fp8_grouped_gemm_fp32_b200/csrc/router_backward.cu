@@ -4,19 +4,21 @@
 // 4 T H E flops against x read once, dx0 read and dx written: at 256 experts the products and the traffic cost
 // about the same, so both products run on the tensor cores and dx is bound by its own traffic.
 //
-//  1. router_prep_w_kernel, router_prep_dl_kernel: fp16 copies for dx, each expert's W_g row scaled by a power
-//     of two so that its largest entry lies in [512, 1024), that power moved into dl, then each token's dl row
-//     scaled likewise (undone in dx's epilogue); dl in three bf16 parts (8 + 8 + 8 bits, all of fp32) for dWg;
-//     partial column sums of dl for db.
-//  2. router_products_kernel, first dx: one fp16 product. fp16 keeps 11 bits, so dx is off by about an eighth
-//     of the step it is rounded with; bf16 parts would need three products for that. A CTA keeps its W_g panel
-//     (all experts x 256 columns) in shared memory and streams token tiles through it (without that the panels
-//     alone would cost more L2 traffic than dx does HBM traffic), the next tile's dx0 loading meanwhile.
-//     Then dWg: the transposed product, x^T (rows h) by the parts of dl, both operands read as they lie in
-//     memory (MN-major), so E is the MMA's N and a few experts cost little. The tensor cores drop bits when they
-//     add to a long sum, so every 128 tokens the sum moves from tensor memory into fp32 registers. The work of
-//     either product is dealt out evenly as one run of units a CTA (or pair); for dWg it leaves one partial tile
-//     per tile it touched, at index tile + its own index (unique: both only rise), and
+//  1. Preparation. dl goes into three bf16 parts (8 + 8 + 8 bits, all of fp32) for dWg, with partial column sums for
+//     db. For dx, up to 128 experts W_g goes into two bf16 parts and dx = d1 w1 + d1 w2 + d2 w1 (error 2^-15; three
+//     products of so few experts hide behind dx's traffic, and nothing has to be known before the parts are made:
+//     one launch). Above, one product has to do: fp16 copies, 11 bits, off by an eighth of the step dx is rounded
+//     with; each expert's W_g row scaled by a power of two so that its largest entry lies in [512, 1024), that power
+//     moved into dl, then each token's dl row scaled likewise (undone in dx's epilogue).
+//  2. router_products_kernel, dx: a CTA keeps its W_g panel (all experts x 256 columns) in shared memory and
+//     streams token tiles through it (without that the panels alone would cost more L2 traffic than dx does HBM
+//     traffic), the next box of dx0 loading meanwhile. dWg: the transposed product, x^T (rows h) by the parts of
+//     dl, both operands read as they lie in memory (MN-major), so E is the MMA's N and a few experts cost little:
+//     up to 64 experts the three parts lie side by side in one N of 48, 96 or 192 (an MMA of N <= 112 takes as
+//     long as one of 112). The tensor cores drop bits when they add to a long sum, so every 128 tokens the sum
+//     moves from tensor memory into fp32 registers. The work of either product is dealt out evenly as one run of
+//     units a CTA (or pair); for dWg it leaves one partial tile per tile it touched, at index tile + its own index
+//     (unique: both only rise), and
 //  3. router_finish_kernel adds the partial tiles in order, and db. No float atomics: results repeat.
 #include <cmath>
 
@@ -49,7 +51,7 @@ __device__ __forceinline__ float2 pow2_scale(float m) {
 }
 
 // ---------------------------------------------------------------- 1. preparation
-// W_g row e -> fp16, scaled; wscale[e] = the inverse of the scale.
+// Above 128 experts: W_g row e -> fp16, scaled; wscale[e] = the inverse of the scale.
 __global__ void __launch_bounds__(256)
 router_prep_w_kernel(const float* __restrict__ Wg, int H, uint16_t* __restrict__ wh, float* __restrict__ wscale) {
     __shared__ float sm[8];
@@ -78,7 +80,92 @@ router_prep_w_kernel(const float* __restrict__ Wg, int H, uint16_t* __restrict__
     }
 }
 
-// dl rows -> fp16 (times the experts' inverse scales, then scaled per token; tscale[t] undoes it), three bf16
+// Up to 128 experts. The first dl_blocks blocks: dl rows -> three bf16 parts side by side, [T][3][pitch] with zeros
+// behind the last expert, and the block's column sums; a warp takes a token at a time, four experts a lane. The
+// others: W_g -> two bf16 parts [2][E][H], 4096 values a block.
+constexpr int kPrepW = 4096;
+
+// The first part holds an infinite or NaN value alone; what is left of a finite one is exact.
+__device__ __forceinline__ float rest_of(float r, uint16_t b) { return fabsf(r) <= 3.0e38f ? r - bf16_bits_to_f32(b) : 0.0f; }
+__device__ __forceinline__ void put4(uint16_t* dst, const uint16_t (&u)[4]) {
+    *reinterpret_cast<uint2*>(dst) = make_uint2(u[0] | static_cast<uint32_t>(u[1]) << 16, u[2] | static_cast<uint32_t>(u[3]) << 16);
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(256)
+router_prep_parts_kernel(const float* __restrict__ dl, const float* __restrict__ Wg, int T, int H, int E, int pitch,
+                         int dl_blocks, uint16_t* __restrict__ parts, float* __restrict__ dbpart, uint16_t* __restrict__ w2) {
+    __shared__ float sm[8][128];
+    dependents_may_launch();
+    wait_for_producers();
+    if (static_cast<int>(blockIdx.x) >= dl_blocks) {
+        const int64_t n = static_cast<int64_t>(E) * H, i0 = static_cast<int64_t>(blockIdx.x - dl_blocks) * kPrepW + threadIdx.x * 4;
+        float4 f[kPrepW / 1024];
+#pragma unroll
+        for (int i = 0; i < kPrepW / 1024; ++i)
+            if (i0 + i * 1024 < n) f[i] = *reinterpret_cast<const float4*>(Wg + i0 + i * 1024);
+#pragma unroll
+        for (int i = 0; i < kPrepW / 1024; ++i)
+            if (i0 + i * 1024 < n) {
+                const float v[4] = {f[i].x, f[i].y, f[i].z, f[i].w};
+                uint16_t b[2][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    b[0][j] = bf16_bits(v[j]);
+                    b[1][j] = bf16_bits(rest_of(v[j], b[0][j]));
+                }
+                put4(w2 + i0 + i * 1024, b[0]);
+                put4(w2 + n + i0 + i * 1024, b[1]);
+            }
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = 4 * lane;
+    const int t0 = blockIdx.x * kPrepTokens + warp;
+    float v[kPrepTokens / 8][4], sum[4] = {};
+#pragma unroll
+    for (int k = 0; k < kPrepTokens / 8; ++k) {
+        const int t = t0 + 8 * k;
+        const float* p = dl + static_cast<int64_t>(t) * E + e;
+        if constexpr (VEC) {
+            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (t < T && e < E) f = *reinterpret_cast<const float4*>(p);
+            v[k][0] = f.x; v[k][1] = f.y; v[k][2] = f.z; v[k][3] = f.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[k][i] = t < T && e + i < E ? p[i] : 0.0f;
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kPrepTokens / 8; ++k) {
+        const int t = t0 + 8 * k;
+        uint16_t b[3][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            sum[i] += v[k][i];
+            float r = v[k][i];
+#pragma unroll
+            for (int p = 0; p < 3; ++p) {
+                b[p][i] = bf16_bits(r);
+                r = rest_of(r, b[p][i]);
+            }
+        }
+        if (t < T && e < pitch) {
+#pragma unroll
+            for (int p = 0; p < 3; ++p) put4(parts + (static_cast<int64_t>(t) * 3 + p) * pitch + e, b[p]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sm[warp][e + i] = sum[i];
+    __syncthreads();
+    if (threadIdx.x < E) {
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s += sm[i][threadIdx.x];
+        dbpart[static_cast<int64_t>(blockIdx.x) * E + threadIdx.x] = s;
+    }
+}
+
+// Above 128 experts. dl rows -> fp16 (times the experts' inverse scales, then scaled per token; tscale[t] undoes it), three bf16
 // parts [3][T][ld], and the block's column sums. A warp takes a token at a time; Q groups of four experts a lane
 // (16-byte reads where E is a multiple of 4).
 template <int Q, bool VEC>
@@ -140,16 +227,12 @@ router_prep_dl_kernel(const float* __restrict__ dl, const float* __restrict__ ws
 #pragma unroll
                     for (int p = 0; p < 3; ++p) {
                         b[p][i] = bf16_bits(r);
-                        // what is left is exact; an infinite or NaN value is carried by its first part alone
-                        r = fabsf(r) <= 3.0e38f ? r - bf16_bits_to_f32(b[p][i]) : 0.0f;
+                        r = rest_of(r, b[p][i]);
                     }
                 }
-                auto put = [](uint16_t* dst, const uint16_t (&u)[4]) {
-                    *reinterpret_cast<uint2*>(dst) = make_uint2(u[0] | static_cast<uint32_t>(u[1]) << 16, u[2] | static_cast<uint32_t>(u[3]) << 16);
-                };
-                put(dlh + at, h);
+                put4(dlh + at, h);
 #pragma unroll
-                for (int p = 0; p < 3; ++p) put(parts + p * plane + at, b[p]);
+                for (int p = 0; p < 3; ++p) put4(parts + p * plane + at, b[p]);
             }
         }
 #pragma unroll
@@ -169,10 +252,11 @@ router_prep_dl_kernel(const float* __restrict__ dl, const float* __restrict__ ws
 // ---------------------------------------------------------------- 2. the products
 // PAIR (above 128 experts): CTA pairs, 256 tokens x 256 columns of dx, 256 columns x 256 experts of dWg. The
 // operand that both halves of a tile need is then held once a pair: 64 KB a stage cross from L2 where single CTAs
-// would load 112 KB for the same MMAs. Otherwise single CTAs, 128 x 256 and 128 x 128. KB: 64-expert blocks of the
-// W_g panel, AS: those of the tokens' ring, NB: dx0 / dx boxes an epilogue warp holds (what the panel leaves room for).
+// would load 112 KB for the same MMAs. Otherwise single CTAs, 128 x 256 and 128 x `pitch` (16, 32, 64 or 128). KB:
+// 64-expert blocks of the W_g panel (of both its parts), AS: those of the tokens' ring, NB: dx0 / dx boxes an epilogue
+// warp holds (what the panel leaves room for).
 // Units are dealt out as runs: group g of G takes [g U / G, (g + 1) U / G).
-constexpr int kDwStages = 5;                                               // barriers; the ring's depth goes by E
+constexpr int kDwStages = 4;                                               // barriers; the ring's depth goes by E
 constexpr int kDwRing = 24 * kRbBox;                                       // its bytes: 192 KB
 constexpr int kDwRegsLow = 40, kDwRegsHigh = 232;                          // as in the grouped GEMM:
 constexpr int kDwRegsSplit = 128 * kDwRegsLow + 256 * kDwRegsHigh;        // what the launch must have allocated
@@ -183,10 +267,11 @@ struct SmemDx {
     uint8_t a[AS][2 * kRbBox];                         // 64 experts of 128 tokens
     uint8_t stage[8][NB][4096];                        // per epilogue warp: 32 rows x 64 columns, bf16
 };
-// dWg's ring: a stage is 64 tokens x 128 columns of x (2 boxes), then 64 tokens x 64 experts of each part (1 or 2
-// boxes a part): 5 boxes where E <= 64, else 8.
+// dWg's ring: a stage is 2 boxes of x (128 columns), then boxes of 64 columns of dl's parts. PAIR: 64 tokens, 2 boxes
+// a part (64 KB); pitch 128 likewise; up to pitch 64 a whole chunk of 128 tokens and 1, 2 or 3 boxes of the parts side by
+// side (48, 64 or 80 KB).
 struct SmemDw {
-    uint8_t ring[kDwRing + kRbBox];
+    uint8_t ring[kDwRing];
 };
 template <bool PAIR, int KB, int AS, int NB>
 struct SmemP {
@@ -212,6 +297,7 @@ struct RouterArgs {
     int has_base;
     int Gx, Gw;               // groups that share dx's units, dWg's units
     int etiles;               // expert tiles of dWg
+    int pitch;                // single CTAs: columns of a part of dl, its experts rounded up
     int Ux, Uw;
     const float* tscale;
     float* part;
@@ -276,11 +362,13 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
     // ======== dWg: unit u = 128-token chunk u % chunks of tile u / chunks
     const int chunks = (g.T + kRbChunk - 1) / kRbChunk;
     const int u0 = grp < g.Gw ? unit_start(g.Uw, g.Gw, grp) : 0, u1 = grp < g.Gw ? unit_start(g.Uw, g.Gw, grp + 1) : 0;
-    const int ebox = PAIR ? 2 : (g.E + 63) / 64;      // 64-expert boxes of each part a CTA loads
-    const uint32_t depth = ebox == 1 ? 5 : 3, stage_bytes = (2 + 3 * ebox) * kRbBox;
-    const uint32_t part_step = ebox * kRbBox / 16;
+    const bool wide = !PAIR && g.pitch <= 64;                           // the parts side by side in one MMA
+    const int ts = wide ? 128 : 64;                                     // tokens of a stage
+    const int dboxes = wide ? (3 * g.pitch + 63) / 64 : 6;
+    const uint32_t box = ts * 128, stage_bytes = (2 + dboxes) * box;
+    const uint32_t depth = kDwRing / stage_bytes;
     auto stage_x = [&](uint32_t s) { return sm.dw.ring + s * stage_bytes; };
-    auto stage_d = [&](uint32_t s, int p) { return sm.dw.ring + s * stage_bytes + (2 + p * ebox) * kRbBox; };
+    auto stage_d = [&](uint32_t s, int i) { return sm.dw.ring + s * stage_bytes + (2 + i) * box; };
 
     // The products are independent: half of the groups begin with dWg, so that dx's traffic and dWg's products run
     // beside each other on the GPU. Between the two a group's MMAs are complete (their accumulators were waited
@@ -306,29 +394,32 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                             have = panel;
                             ++panels;
                             const int c0 = panel * 256 + static_cast<int>(rank) * 128;
-                            if (rank == 0) mbar_arrive_expect_tx(&sm.wfull, (PAIR ? 2u : 1u) * kblocks * kWBoxes * kRbBox);
-                            for (int kb = 0; kb < kblocks; ++kb)
+                            // PAIR: this CTA's half of the panel; else both parts of all of it
+                            const int blocks = PAIR ? kblocks : 2 * kblocks;
+                            if (rank == 0) mbar_arrive_expect_tx(&sm.wfull, (PAIR ? 2u : 1u) * blocks * kWBoxes * kRbBox);
+                            for (int kb = 0; kb < blocks; ++kb)
                                 for (int i = 0; i < kWBoxes; ++i) {
                                     if constexpr (PAIR)
-                                        tma_load_2d_pair(sm.dx.w[kb] + i * kRbBox, &tm_w, leader_bar(&sm.wfull), c0 + 64 * i, kb * 64);
+                                        tma_load_3d_pair(sm.dx.w[kb] + i * kRbBox, &tm_w, leader_bar(&sm.wfull), c0 + 64 * i, kb * 64, 0);
                                     else
-                                        tma_load_2d(sm.dx.w[kb] + i * kRbBox, &tm_w, &sm.wfull, c0 + 64 * i, kb * 64);
+                                        tma_load_3d(sm.dx.w[kb] + i * kRbBox, &tm_w, &sm.wfull, c0 + 64 * i, (kb >> 1) * 64, kb & 1);
                                 }
                         }
-                        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                        // PAIR: the tile's fp16 dl; else its first part and its second, block by block
+                        for (int kb = 0; kb < (PAIR ? kblocks : 2 * kblocks); ++kb, ++it) {
                             const int s = it % AS;
                             if (!mbar_wait(&sm.aempty[s], ((it / AS) & 1) ^ 1, kRbWaitNs)) { fail(); ok = false; break; }
                             if (rank == 0) mbar_arrive_expect_tx(&sm.afull[s], (PAIR ? 2u : 1u) * 2 * kRbBox);
                             if constexpr (PAIR)
                                 tma_load_2d_pair(sm.dx.a[s], &tm_dl, leader_bar(&sm.afull[s]), kb * 64, tile * kTok + static_cast<int>(rank) * 128);
                             else
-                                tma_load_2d(sm.dx.a[s], &tm_dl, &sm.afull[s], kb * 64, tile * kTok);
+                                tma_load_2d(sm.dx.a[s], &tm_dl, &sm.afull[s], (kb & 1) * g.pitch + (kb >> 1) * 64, tile * kTok);
                         }
                     }
                 } else if (warp == 1 && lane == 0 && rank == 0) {
                     uint32_t it = 0, ti = 0, panels = 0;
                     int have = -1;
-                    const uint32_t idesc = f16_idesc(kTok, 256, false, false, true);
+                    const uint32_t idesc = f16_idesc(kTok, 256, !PAIR, false, true);
                     bool ok = !sm.abort_flag;
                     for (int u = x0; ok && u < x1 && !sm.abort_flag; ++u, ++ti) {
                         const int panel = u / ttiles;
@@ -340,15 +431,22 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                         const uint32_t buf = ti & 1, d = tmem + buf * 256;
                         if (!mbar_wait(&sm.tempty[0][buf], ((ti >> 1) & 1) ^ 1, kRbWaitNs)) { fail(); break; }
                         tc_fence_after();
-                        for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                        for (int kb = 0; kb < (PAIR ? kblocks : 2 * kblocks); ++kb, ++it) {
                             const int s = it % AS;
                             if (!mbar_wait(&sm.afull[s], (it / AS) & 1, kRbWaitNs)) { fail(); ok = false; break; }
                             tc_fence_after();
-                            const uint64_t da = sw128_kmajor_desc(smem_u32(sm.dx.a[s])), db = sw128_mnmajor_desc(smem_u32(sm.dx.w[kb]), kRbBox);
+                            // 16 experts on (the descriptors hold address / 16): 32 bytes in a row, 2048 in the panel
+                            const uint64_t da = sw128_kmajor_desc(smem_u32(sm.dx.a[s]));
+                            const uint64_t db = sw128_mnmajor_desc(smem_u32(sm.dx.w[PAIR ? kb : kb & ~1]), kRbBox);
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {           // 16 experts: 32 bytes on in a row, 2048 in the panel
+                            for (int kk = 0; kk < 4; ++kk) {
                                 if constexpr (PAIR) umma_f16_pair(d, da + kk * 2, db + kk * 128, idesc, kb + kk > 0);
                                 else umma_f16(d, da + kk * 2, db + kk * 128, idesc, kb + kk > 0);
+                            }
+                            if (!PAIR && !(kb & 1)) {              // the first part of dl also meets the second of W_g
+                                const uint64_t d2 = sw128_mnmajor_desc(smem_u32(sm.dx.w[kb | 1]), kRbBox);
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) umma_f16(d, da + kk * 2, d2 + kk * 128, idesc, 1);
                             }
                             if constexpr (PAIR) umma_commit_pair(&sm.aempty[s], 0x3); else umma_commit(&sm.aempty[s]);
                         }
@@ -369,45 +467,48 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                         const int tile = u / chunks, t0 = (u - tile * chunks) * kRbChunk;
                         const int h0 = tile / g.etiles * kRows + static_cast<int>(rank) * 128;
                         const int e0 = tile % g.etiles * kCols + static_cast<int>(rank) * 128;
-                        for (int t = t0; t < min(t0 + kRbChunk, g.T); t += 64, ++it) {
+                        for (int t = t0; t < min(t0 + kRbChunk, g.T); t += ts, ++it) {
                             const uint32_t s = it % depth;
                             if (!mbar_wait(&sm.empty[s], ((it / depth) & 1) ^ 1, kRbWaitNs)) { fail(); ok = false; break; }
                             if (rank == 0) mbar_arrive_expect_tx(&sm.full[s], bytes);
                             if constexpr (PAIR) {
                                 const uint32_t fb = leader_bar(&sm.full[s]);
-                                for (int i = 0; i < 2; ++i) tma_load_3d_pair(stage_x(s) + i * kRbBox, &tm_x, fb, h0 + 64 * i, t, 0);
-                                for (int p = 0; p < 3; ++p)
-                                    for (int i = 0; i < 2; ++i) tma_load_3d_pair(stage_d(s, p) + i * kRbBox, &tm_d, fb, e0 + 64 * i, t, p);
+                                for (int i = 0; i < 2; ++i) tma_load_3d_pair(stage_x(s) + i * box, &tm_x, fb, h0 + 64 * i, t, 0);
+                                for (int i = 0; i < 6; ++i) tma_load_3d_pair(stage_d(s, i), &tm_d, fb, e0 + 64 * (i & 1), t, i >> 1);
                             } else {
-                                for (int i = 0; i < 2; ++i) tma_load_3d(stage_x(s) + i * kRbBox, &tm_x, &sm.full[s], h0 + 64 * i, t, 0);
-                                for (int p = 0; p < 3; ++p)
-                                    for (int i = 0; i < ebox; ++i) tma_load_3d(stage_d(s, p) + i * kRbBox, &tm_d, &sm.full[s], e0 + 64 * i, t, p);
+                                for (int i = 0; i < 2; ++i) tma_load_3d(stage_x(s) + i * box, &tm_x, &sm.full[s], h0 + 64 * i, t, 0);
+                                for (int i = 0; i < dboxes; ++i) tma_load_3d(stage_d(s, i), &tm_d, &sm.full[s], 64 * i, t, 0);
                             }
                         }
                     }
                 } else if (warp == 1 && lane == 0 && rank == 0) {
                     uint32_t it = 0, ci = 0;
                     bool ok = !sm.abort_flag;
-                    const uint32_t idesc = f16_idesc(kRows, PAIR ? 256 : (g.E + 15) / 16 * 16, true, true, true);
+                    const uint32_t idesc = f16_idesc(kRows, PAIR ? 256 : wide ? 3 * g.pitch : 128, true, true, true);
                     for (int u = u0; ok && u < u1 && !sm.abort_flag; ++u, ++ci) {
                         const int t0 = u % chunks * kRbChunk;
                         const uint32_t buf = ci & 1, d = tmem + buf * 256;
                         if (!mbar_wait(&sm.tempty[1][buf], ((ci >> 1) & 1) ^ 1, kRbWaitNs)) { fail(); break; }
                         tc_fence_after();
-                        for (int t = t0; t < min(t0 + kRbChunk, g.T); t += 64, ++it) {
+                        for (int t = t0; t < min(t0 + kRbChunk, g.T); t += ts, ++it) {
                             const uint32_t s = it % depth;
                             if (!mbar_wait(&sm.full[s], (it / depth) & 1, kRbWaitNs)) { fail(); ok = false; break; }
                             tc_fence_after();
-                            // the descriptors' low bits hold address / 16: a slice of 16 tokens is 2048 bytes on. The three
-                            // parts of a slice share x, which the tensor core then reads once
-                            const uint64_t da = sw128_mnmajor_desc(smem_u32(stage_x(s)), kRbBox);
-                            const uint64_t db = sw128_mnmajor_desc(smem_u32(stage_d(s, 0)), kRbBox);
+                            // the descriptors hold address / 16: a slice of 16 tokens is 2048 bytes on
+                            const uint64_t da = sw128_mnmajor_desc(smem_u32(stage_x(s)), box);
+                            const uint64_t db = sw128_mnmajor_desc(smem_u32(stage_d(s, 0)), box);
+                            if (wide) {
 #pragma unroll
-                            for (int kk = 0; kk < 4; ++kk) {
-                                const uint64_t a = da + kk * 128, b = db + kk * 128;
-                                umma_f16_keep<PAIR, KeepA::kFill>(d, a, b, idesc, kk > 0 || t > t0);
-                                umma_f16_keep<PAIR, KeepA::kUse>(d, a, b + part_step, idesc, 1);
-                                umma_f16_keep<PAIR, KeepA::kLast>(d, a, b + 2 * part_step, idesc, 1);
+                                for (int kk = 0; kk < 8; ++kk) umma_f16(d, da + kk * 128, db + kk * 128, idesc, kk > 0);
+                            } else {
+                                // the three parts of a slice share x, which the tensor core then reads once
+#pragma unroll
+                                for (int kk = 0; kk < 4; ++kk) {
+                                    const uint64_t a = da + kk * 128, b = db + kk * 128;
+                                    umma_f16_keep<PAIR, KeepA::kFill>(d, a, b, idesc, kk > 0 || t > t0);
+                                    umma_f16_keep<PAIR, KeepA::kUse>(d, a, b + 2 * kRbBox / 16, idesc, 1);
+                                    umma_f16_keep<PAIR, KeepA::kLast>(d, a, b + 4 * kRbBox / 16, idesc, 1);
+                                }
                             }
                             if constexpr (PAIR) umma_commit_pair(&sm.empty[s], 0x3); else umma_commit(&sm.empty[s]);
                         }
@@ -439,13 +540,13 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                     tma_load_2d(sm.dx.stage[ew][j % NB], &tm_in, bar, col0, row0);
                 };
                 if (g.has_base && lane == 0 && boxes > 0 && !sm.abort_flag) fetch(0);
-                float sc = 0.0f;
+                float sc = 1.0f;                       // undoes the token's scale
                 for (uint32_t j = 0; j < boxes; ++j) {
                     if (sm.abort_flag) break;
                     const uint32_t ti = j >> 1, buf = ti & 1, n = j % NB;
                     int row0, col0;
                     place(j, row0, col0);
-                    if (!(j & 1)) sc = row0 + lane < g.T ? g.tscale[row0 + lane] : 0.0f;
+                    if (PAIR && !(j & 1)) sc = row0 + lane < g.T ? g.tscale[row0 + lane] : 0.0f;
                     if (lane == 0) {
                         bulk_wait_read<NB - 2>();      // box j + 1 - NB has left the buffer that box j + 1 goes to
                         if (g.has_base && j + 1 < boxes) fetch(j + 1);
@@ -498,9 +599,10 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                 }
                 if (lane == 0) bulk_wait_read_all();
             } else {
-                // promotion: warp = lane quadrant q x half of the experts' columns
-                constexpr int kMine = kCols / 2;
+                // promotion: warp = lane quadrant q x half of the experts
+                constexpr int kMine = PAIR ? 128 : 64;
                 const int q = warp & 3, half = (warp - 4) >> 2;
+                const int mine = PAIR ? kMine : g.pitch / 2, cols = PAIR ? kCols : g.pitch;
                 float acc[kMine];
                 uint32_t ci = 0;
                 for (int u = u0; u < u1; ++u, ++ci) {
@@ -514,25 +616,46 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                     const uint32_t buf = ci & 1;
                     if (!mbar_wait(&sm.tfull[1][buf], (ci >> 1) & 1, kRbWaitNs)) { fail(); break; }
                     tc_fence_after();
-                    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * kMine;
+                    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * mine;
+                    if (!wide) {
 #pragma unroll
-                    for (int c = 0; c < kMine / 32; ++c) {
-                        float v[32];
-                        tmem_ld32(taddr + 32 * c, v);
-                        tmem_ld_wait();
+                        for (int c = 0; c < kMine / 32; ++c) {
+                            float v[32];
+                            tmem_ld32(taddr + 32 * c, v);
+                            tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) acc[32 * c + i] += v[i];
+                            for (int i = 0; i < 32; ++i) acc[32 * c + i] += v[i];
+                        }
+                    } else if (g.pitch == 64) {
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) {
+                            float v[32];
+                            tmem_ld32(taddr + 64 * p, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) acc[i] += v[i];
+                        }
+                    } else {
+                        // 16 columns of each part (at pitch 16 the upper 8 are another warp's or nobody's, and not kept)
+#pragma unroll
+                        for (int p = 0; p < 3; ++p) {
+                            float v[16];
+                            tmem_ld16(taddr + g.pitch * p, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) acc[i] += v[i];
+                        }
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) release(&sm.tempty[1][buf]);
                     if (end) {
-                        // partial tile [kCols][kRows]: a warp's store is 32 consecutive rows of one expert
-                        float* dst = g.part + (static_cast<int64_t>(tile) + grp) * kCols * kRows + rank * 128 + q * 32 + lane;
-                        const int ecount = g.E - tile % g.etiles * kCols;
+                        // partial tile [cols][kRows]: a warp's store is 32 consecutive rows of one expert
+                        float* dst = g.part + (static_cast<int64_t>(tile) + grp) * cols * kRows + rank * 128 + q * 32 + lane;
+                        const int ecount = min(g.E - tile % g.etiles * cols, (half + 1) * mine);
 #pragma unroll
                         for (int i = 0; i < kMine; ++i)
-                            if (half * kMine + i < ecount) dst[(half * kMine + i) * kRows] = acc[i];
+                            if (half * mine + i < ecount) dst[(half * mine + i) * kRows] = acc[i];
                     }
                 }
             }
@@ -738,7 +861,7 @@ RbPlan plan_of(int T, int H, int E) {
     RbPlan p;
     p.pair = E > 128;
     p.rows = p.pair ? 256 : 128;
-    p.cols = p.pair ? 256 : 128;
+    p.cols = p.pair ? 256 : E <= 16 ? 16 : E <= 32 ? 32 : E <= 64 ? 64 : 128;
     p.htiles = (H + p.rows - 1) / p.rows;
     p.etiles = (E + p.cols - 1) / p.cols;
     p.chunks = (T + kRbChunk - 1) / kRbChunk;
@@ -748,11 +871,11 @@ RbPlan plan_of(int T, int H, int E) {
 }
 
 struct RbWs {
-    uint16_t* wh;
-    float* wscale;
-    uint16_t* dlh;
-    float* tscale;
-    uint16_t* parts;
+    uint16_t* wh;        // W_g: fp16 [E][H] (pairs), else two bf16 parts [2][E][H]
+    float* wscale;       // pairs
+    uint16_t* dlh;       // pairs: dl in fp16 [T][ld]
+    float* tscale;       // pairs
+    uint16_t* parts;     // dl in bf16 parts: [3][T][ld] (pairs), else [T][3][pitch]
     float* dbpart;
     float* part;
     size_t total;
@@ -769,11 +892,11 @@ RbWs carve_router(int T, int H, int E, void* base) {
         off += (bytes + 255) / 256 * 256;
         return r;
     };
-    w.wh = reinterpret_cast<uint16_t*>(take(2ull * E * H));
-    w.wscale = reinterpret_cast<float*>(take(4ull * E));
-    w.dlh = reinterpret_cast<uint16_t*>(take(2ull * T * ld));
-    w.tscale = reinterpret_cast<float*>(take(4ull * T));
-    w.parts = reinterpret_cast<uint16_t*>(take(6ull * T * ld));
+    w.wh = reinterpret_cast<uint16_t*>(take((pl.pair ? 2ull : 4ull) * E * H));
+    w.wscale = reinterpret_cast<float*>(take(pl.pair ? 4ull * E : 0));
+    w.dlh = reinterpret_cast<uint16_t*>(take(pl.pair ? 2ull * T * ld : 0));
+    w.tscale = reinterpret_cast<float*>(take(pl.pair ? 4ull * T : 0));
+    w.parts = reinterpret_cast<uint16_t*>(take(6ull * T * (pl.pair ? ld : pl.cols)));
     w.dbpart = reinterpret_cast<float*>(take(4ull * ((T + kPrepTokens - 1) / kPrepTokens) * E));
     w.part = reinterpret_cast<float*>(take(4ull * (static_cast<size_t>(pl.htiles) * pl.etiles + pl.most_groups) * pl.rows * pl.cols));
     w.total = off;
@@ -883,18 +1006,28 @@ moe_status_t moe_router_backward(int T, int H, int E, const void* x, const float
                    : MOE_ERR_CUDA;
     TileGroups tg = {};
     if (T > 0) {
-        if (!ok(launch_dependent(router_prep_w_kernel, dim3(E), dim3(256), 0, s, Wg, H, w.wh, w.wscale))) return MOE_ERR_CUDA;
         const bool vec = E % 4 == 0;
-        auto prep = E <= 128   ? (vec ? router_prep_dl_kernel<1, true> : router_prep_dl_kernel<1, false>)
-                    : E <= 256 ? (vec ? router_prep_dl_kernel<2, true> : router_prep_dl_kernel<2, false>)
-                               : (vec ? router_prep_dl_kernel<4, true> : router_prep_dl_kernel<4, false>);
-        if (!ok(launch_dependent(prep, dim3(db_blocks), dim3(256), 0, s, dlogits, w.wscale, T, E, ld, w.dlh, w.tscale, w.parts, w.dbpart)))
-            return MOE_ERR_CUDA;
         CUtensorMap m[6];
-        if (!make_map16(&m[0], w.dlh, false, E, T, 1, ld, 128, 2) || !make_map16(&m[1], w.wh, false, H, E, 1, H, 64, 2) ||
-            !make_map16(&m[2], dx0 ? dx0 : dx, true, H, T, 1, H, 32, 2) || !make_map16(&m[3], dx, true, H, T, 1, H, 32, 2) ||
-            !make_map16(&m[4], x, true, H, T, 1, H, 64, 3) || !make_map16(&m[5], w.parts, true, E, T, 3, ld, 64, 3))
-            return MOE_ERR_CUDA;
+        bool mapped = make_map16(&m[2], dx0 ? dx0 : dx, true, H, T, 1, H, 32, 2) && make_map16(&m[3], dx, true, H, T, 1, H, 32, 2);
+        if (p.pair) {
+            auto prep = E <= 256 ? (vec ? router_prep_dl_kernel<2, true> : router_prep_dl_kernel<2, false>)
+                                 : (vec ? router_prep_dl_kernel<4, true> : router_prep_dl_kernel<4, false>);
+            if (!ok(launch_dependent(router_prep_w_kernel, dim3(E), dim3(256), 0, s, Wg, H, w.wh, w.wscale)) ||
+                !ok(launch_dependent(prep, dim3(db_blocks), dim3(256), 0, s, dlogits, w.wscale, T, E, ld, w.dlh, w.tscale, w.parts, w.dbpart)))
+                return MOE_ERR_CUDA;
+            mapped = mapped && make_map16(&m[0], w.dlh, false, E, T, 1, ld, 128, 2) &&
+                     make_map16(&m[1], w.wh, false, H, E, 1, H, 64, 3) && make_map16(&m[4], x, true, H, T, 1, H, 64, 3) &&
+                     make_map16(&m[5], w.parts, true, E, T, 3, ld, 64, 3);
+        } else {
+            const int w_blocks = static_cast<int>((static_cast<int64_t>(E) * H + kPrepW - 1) / kPrepW), ts = p.cols <= 64 ? 128 : 64;
+            if (!ok(launch_dependent(vec ? router_prep_parts_kernel<true> : router_prep_parts_kernel<false>, dim3(db_blocks + w_blocks),
+                                     dim3(256), 0, s, dlogits, Wg, T, H, E, p.cols, db_blocks, w.parts, w.dbpart, w.wh)))
+                return MOE_ERR_CUDA;
+            mapped = mapped && make_map16(&m[0], w.parts, true, 3 * p.cols, T, 1, 3 * p.cols, 128, 2) &&
+                     make_map16(&m[1], w.wh, true, H, E, 2, H, 64, 3) && make_map16(&m[4], x, true, H, T, 1, H, ts, 3) &&
+                     make_map16(&m[5], w.parts, true, 3 * p.cols, T, 1, 3 * p.cols, ts, 3);
+        }
+        if (!mapped) return MOE_ERR_CUDA;
         RouterArgs g;
         g.T = T;
         g.H = H;
@@ -910,11 +1043,13 @@ moe_status_t moe_router_backward(int T, int H, int E, const void* x, const float
             tg.last[t] = static_cast<uint8_t>(group_of(g.Uw, g.Gw, (t + 1) * p.chunks - 1));
         }
         g.etiles = p.etiles;
+        g.pitch = p.cols;
         g.tscale = w.tscale;
         g.part = w.part;
         g.status = status;
         const int used = std::max(g.Gx, g.Gw);
-        const cudaError_t err = !p.pair    ? launch_products<false, 2, 4, 3>(m, g, used, s)
+        const cudaError_t err = E <= 64    ? launch_products<false, 2, 4, 3>(m, g, used, s)
+                                : E <= 128 ? launch_products<false, 4, 2, 2>(m, g, used, s)
                                 : E <= 256 ? launch_products<true, 4, 4, 3>(m, g, used, s)
                                            : launch_products<true, 8, 2, 2>(m, g, used, s);
         if (!ok(err)) return MOE_ERR_CUDA;
