@@ -16,6 +16,11 @@
 // so X is carried as the sum of two fp16 values (22 bits): the first feeds the products, both enter a X in
 // the epilogue. That costs no tensor work and leaves the result closer than the rounding of O to bf16.
 // X is stored times a power of two near sqrt(l) (entries near 1), A and B times 64.
+//
+// Large matrices with l >= 1.5 s take their first two steps at once: X_2 = (a I + B_2)(a I + B_1) X_0 with A_2 =
+// (a I + B_1)^2 A_1, all in s x s products, 3 s^2 l + 5 s^3 flops instead of 6 s^2 l + 2 s^3 (a fifth to a third
+// less for these two). A later pair must not: A_2 then carries A_1's rounding noise, grown by a^2, into directions
+// that the products with X would have resolved (2 to 3 times the error); in the first pair it does not show.
 #include <cmath>
 
 #include <algorithm>
@@ -63,19 +68,30 @@ struct SmemO {
 };
 
 // Tensor maps over a wave's buffers, [matrices][rows][columns] of fp16: operand boxes of 64 x 64 values,
-// epilogue boxes of 64 columns x 32 rows and, for transposed stores, 32 columns x 64 rows.
+// epilogue boxes of 64 columns x 32 rows and, for transposed stores, 32 columns x 64 rows. hi: both buffers of X's first
+// parts, matrix b of buffer i at i * mats + b; sq: the s x s matrices, slot i at i * mats + b.
 struct OrthoMaps {
-    CUtensorMap hi_op[2], hi_ep[2], lo_ep;
-    CUtensorMap p_op, p_ep, p_tr;            // 64 A
-    CUtensorMap q_op, q_ep, q_tr;            // 64 B
+    CUtensorMap hi_op, hi_ep, lo_ep;
+    CUtensorMap sq_op, sq_ep, sq_tr;
 };
 
+// out = cxy X Y + cu U + cv V on slots of symmetric matrices (u, v: -1 for none; all are stored times 64).
+struct OrthoSym {
+    int x, y, u, v, out;
+    float cxy, cu, cv;
+};
+
+// The iteration as groups of products: A (slot 0) from X, then nsym symmetric products, then the update X <- ca X + Q X
+// with Q in slot 1. The first group may be two steps in one.
+constexpr int kSlots = 6, kMostSym = 5;
 struct OrthoArgs {
     int M, N;                // rows and columns of a matrix
     int mats;                // matrices of the wave
-    int steps;
+    int groups;
     int interleaved;
-    float a, b, c;
+    int nsym0;               // symmetric products of the first group (1 or 5); the others have one
+    OrthoSym sym0[kMostSym], sym;
+    float ca0, ca;
     float out_scale;         // scale / the power of two X is stored with
     float gram_scale;        // 64 / that power squared
     uint16_t* O;             // the wave's first matrix
@@ -83,9 +99,12 @@ struct OrthoArgs {
     int* status;
 };
 
-// One tile of one product: matrix b, product 0 = A, 1 = B, 2 = the update, of step `step`.
+// One tile of one product: matrix b, product 0 = A, 1 .. nsym symmetric, nsym + 1 = the update.
+enum OrthoKind { kGram, kSym, kUpdate };
 struct OrthoTile {
-    int step, prod, b, ti, tj;
+    int group, b, ti, tj;
+    OrthoKind kind;
+    const OrthoSym* sym;
 };
 
 template <bool PAIR>
@@ -110,27 +129,31 @@ template <bool PAIR>
 struct OrthoWalk {
     const OrthoArgs& g;
     const OrthoShape<PAIR>& sh;
-    int pos, step, prod, stride;
+    int pos, group, prod, stride;
+    int before;                            // tiles of a matrix in the products before this one
     __device__ OrthoWalk(const OrthoArgs& g_, const OrthoShape<PAIR>& sh_, int first, int stride_)
-        : g(g_), sh(sh_), pos(first), step(0), prod(0), stride(stride_) {
+        : g(g_), sh(sh_), pos(first), group(0), prod(0), stride(stride_), before(0) {
         settle();
     }
-    __device__ int per_matrix() const { return prod == 2 ? sh.nu : sh.ns; }
+    __device__ int nsym() const { return group == 0 ? g.nsym0 : 1; }
+    __device__ int per_matrix() const { return prod > nsym() ? sh.nu : sh.ns; }
     __device__ void settle() {
-        while (step < g.steps && pos >= g.mats * per_matrix()) {
+        while (group < g.groups && pos >= g.mats * per_matrix()) {
             pos -= g.mats * per_matrix();
-            if (++prod == 3) { prod = 0; ++step; }
+            before += per_matrix();
+            if (prod > nsym()) { prod = 0; ++group; } else { ++prod; }
         }
     }
-    __device__ bool more() const { return step < g.steps; }
+    __device__ bool more() const { return group < g.groups; }
     __device__ void next() { pos += stride; settle(); }
     __device__ OrthoTile tile() const {
         OrthoTile t;
-        t.step = step;
-        t.prod = prod;
+        t.group = group;
+        t.kind = prod == 0 ? kGram : prod > nsym() ? kUpdate : kSym;
+        t.sym = group == 0 ? &g.sym0[t.kind == kSym ? prod - 1 : 0] : &g.sym;
         t.b = pos / per_matrix();
         const int i = pos - t.b * per_matrix();
-        if (prod == 2) {
+        if (t.kind == kUpdate) {
             // the shorter side runs fastest: neighbours share the longer operand's panel
             if (sh.tall) { t.ti = i / sh.cb; t.tj = i - t.ti * sh.cb; }
             else { t.tj = i / sh.rb; t.ti = i - t.tj * sh.rb; }
@@ -145,11 +168,13 @@ struct OrthoWalk {
     }
     // Finished tiles (each CTA of a pair counts its half) its matrix needs before this tile may start: all
     // earlier products'.
-    __device__ unsigned needs() const {
-        const int tiles = step * (2 * sh.ns + sh.nu) + prod * sh.ns;
-        return static_cast<unsigned>(tiles) * (PAIR ? 2 : 1);
-    }
+    __device__ unsigned needs() const { return static_cast<unsigned>(before) * (PAIR ? 2 : 1); }
 };
+
+// Whether both operands of a tile are the same rows (a diagonal tile of A or of a square).
+__device__ __forceinline__ bool same_rows(const OrthoTile& t) {
+    return t.ti == t.tj && (t.kind == kGram || (t.kind == kSym && t.sym->x == t.sym->y));
+}
 
 __device__ __forceinline__ uint32_t pack_half2(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
@@ -234,14 +259,18 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                 const OrthoTile t = w.tile();
                 if (!wait_for(t.b, w.needs())) { fail(); break; }
                 mbar_arrive(&sm.ready[ti % kOReady]);                  // for the epilogue warps' loads of this tile
-                const int cur = t.step & 1;
-                // product 0: X X^T (X^T X); 1: A A; 2: B X (X B)
-                const CUtensorMap* ma = t.prod == 0 ? &maps.hi_op[cur] : t.prod == 1 ? &maps.p_op : sh.tall ? &maps.hi_op[cur] : &maps.q_op;
-                const CUtensorMap* mb = t.prod == 0 ? &maps.hi_op[cur] : t.prod == 1 ? &maps.p_op : sh.tall ? &maps.q_op : &maps.hi_op[cur];
-                const bool a_mn = t.prod == 0 && sh.tall;
-                const bool b_mn = (t.prod == 0 && sh.tall) || (t.prod == 2 && !sh.tall);
-                const int K = t.prod == 0 ? sh.l : sh.s;
-                const bool same = t.prod != 2 && t.ti == t.tj;   // a diagonal tile: both operands are the same rows
+                // A: X X^T (X^T X); symmetric: X Y of their slots; update: Q X (X Q)
+                const int hz = (t.group & 1) * g.mats + t.b;
+                const bool a_hi = t.kind == kGram || (t.kind == kUpdate && sh.tall);
+                const bool b_hi = t.kind == kGram || (t.kind == kUpdate && !sh.tall);
+                const CUtensorMap* ma = a_hi ? &maps.hi_op : &maps.sq_op;
+                const CUtensorMap* mb = b_hi ? &maps.hi_op : &maps.sq_op;
+                const int za = a_hi ? hz : (t.kind == kUpdate ? 1 : t.sym->x) * g.mats + t.b;
+                const int zb = b_hi ? hz : (t.kind == kUpdate ? 1 : t.sym->y) * g.mats + t.b;
+                const bool a_mn = t.kind == kGram && sh.tall;
+                const bool b_mn = (t.kind == kGram && sh.tall) || (t.kind == kUpdate && !sh.tall);
+                const int K = t.kind == kGram ? sh.l : sh.s;
+                const bool same = same_rows(t);
                 const int ra = t.ti * kEdge + static_cast<int>(rank) * 128, rb = t.tj * kEdge + static_cast<int>(rank) * 128;
                 for (int k0 = 0; k0 < K; k0 += kOK, ++it) {
                     const int s = it % kOStages;
@@ -252,11 +281,11 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                     for (int i = 0; i < 2; ++i) {
                         const int ya = ra + 64 * i, yb = rb + 64 * i;
                         if constexpr (PAIR) {
-                            tma_load_3d_pair(sm.a[s] + i * kOBox, ma, fb, a_mn ? ya : k0, a_mn ? k0 : ya, t.b);
-                            if (!same) tma_load_3d_pair(sm.b[s] + i * kOBox, mb, fb, b_mn ? yb : k0, b_mn ? k0 : yb, t.b);
+                            tma_load_3d_pair(sm.a[s] + i * kOBox, ma, fb, a_mn ? ya : k0, a_mn ? k0 : ya, za);
+                            if (!same) tma_load_3d_pair(sm.b[s] + i * kOBox, mb, fb, b_mn ? yb : k0, b_mn ? k0 : yb, zb);
                         } else {
-                            tma_load_3d(sm.a[s] + i * kOBox, ma, &sm.full[s], a_mn ? ya : k0, a_mn ? k0 : ya, t.b);
-                            if (!same) tma_load_3d(sm.b[s] + i * kOBox, mb, &sm.full[s], b_mn ? yb : k0, b_mn ? k0 : yb, t.b);
+                            tma_load_3d(sm.a[s] + i * kOBox, ma, &sm.full[s], a_mn ? ya : k0, a_mn ? k0 : ya, za);
+                            if (!same) tma_load_3d(sm.b[s] + i * kOBox, mb, &sm.full[s], b_mn ? yb : k0, b_mn ? k0 : yb, zb);
                         }
                     }
                 }
@@ -269,9 +298,10 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
             bool ok = true;
             for (; ok && w.more() && !sm.abort_flag; w.next(), ++ti) {
                 const OrthoTile t = w.tile();
-                const bool a_mn = t.prod == 0 && sh.tall;
-                const bool b_mn = (t.prod == 0 && sh.tall) || (t.prod == 2 && !sh.tall);
-                const int K = t.prod == 0 ? sh.l : sh.s;
+                const bool a_mn = t.kind == kGram && sh.tall;
+                const bool b_mn = (t.kind == kGram && sh.tall) || (t.kind == kUpdate && !sh.tall);
+                const int K = t.kind == kGram ? sh.l : sh.s;
+                const bool same = same_rows(t);
                 const uint32_t idesc = f16_idesc(kEdge, kEdge, false, a_mn, b_mn);
                 const uint32_t a_step = a_mn ? 128 : 2, b_step = b_mn ? 128 : 2;
                 const uint32_t buf = ti & 1, d = tmem + buf * kEdge;
@@ -284,7 +314,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                     // 16 K values on (the descriptors hold address / 16): 32 bytes in a K-major row, 16 rows of 128 bytes
                     // of an MN-major box
                     uint64_t da = a_mn ? sw128_mnmajor_desc(smem_u32(sm.a[s]), kOBox) : sw128_kmajor_desc(smem_u32(sm.a[s]));
-                    const uint32_t b0 = smem_u32(t.prod != 2 && t.ti == t.tj ? sm.a[s] : sm.b[s]);
+                    const uint32_t b0 = smem_u32(same ? sm.a[s] : sm.b[s]);
                     uint64_t db = b_mn ? sw128_mnmajor_desc(b0, kOBox) : sw128_kmajor_desc(b0);
 #pragma unroll
                     for (int kk = 0; kk < kOK / 16; ++kk, da += a_step, db += b_step) {
@@ -302,7 +332,6 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
         const uint32_t st0 = smem_u32(sm.stage[ew][0]), st1 = smem_u32(sm.stage[ew][1]);
         const uint32_t tempty0 = PAIR ? mapa_shared(smem_u32(&sm.tempty[0]), 0) : 0u;
         constexpr int kSubs = kEdge / 128;
-        const float quad = g.c * (1.0f / kPScale), inv = 1.0f / kPScale;
         uint32_t ti = 0, loads = 0, tiles = 0;
         bool ok = true;
         for (; ok && w.more(); w.next(), ++ti) {
@@ -310,10 +339,15 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
             const OrthoTile t = w.tile();
             const uint32_t buf = ti & 1;
             const int row0 = t.ti * kEdge + static_cast<int>(rank) * 128 + q * 32;
-            const int rows = t.prod == 2 ? g.M : sh.s, cols = t.prod == 2 ? g.N : sh.s;
-            const int cur = t.step & 1;
-            const bool last = t.prod == 2 && t.step == g.steps - 1;
-            const bool mirror = t.prod != 2 && t.ti != t.tj;
+            const bool update = t.kind == kUpdate;
+            const int rows = update ? g.M : sh.s, cols = update ? g.N : sh.s;
+            const int cur = t.group & 1;
+            const bool last = update && t.group == g.groups - 1;
+            const bool mirror = !update && t.ti != t.tj;
+            // what comes in: X's two parts, or a symmetric product's addends
+            const bool in0 = update || (t.kind == kSym && t.sym->u >= 0), in1 = update || (t.kind == kSym && t.sym->v >= 0);
+            const float ca = t.group == 0 ? g.ca0 : g.ca, inv = 1.0f / kPScale;
+            const float cxy = t.kind == kGram ? g.gram_scale : t.sym->cxy, cu = t.sym->cu, cv = t.sym->cv;
 #pragma unroll 1
             for (int sub = 0; sub < kSubs; ++sub) {
                 const int col0 = t.tj * kEdge + half * (kEdge / 2) + sub * 64;
@@ -321,19 +355,19 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                 int good = 1;
                 if (lane == 0) {
                     bulk_wait_read_all();
-                    if (t.prod != 0) {
+                    if (in0 || in1) {
                         if (sub == 0) {
                             good = mbar_wait(&sm.ready[ti % kOReady], (ti / kOReady) & 1, kOrthoWaitNs);
                             fence_proxy_async();
                         }
                         if (good) {
-                            mbar_arrive_expect_tx(&sm.eload[ew], t.prod == 1 ? 4096 : 8192);
-                            if (t.prod == 1) {
-                                tma_load_3d(sm.stage[ew][0], &maps.p_ep, &sm.eload[ew], col0, row0, t.b);
-                            } else {
-                                tma_load_3d(sm.stage[ew][0], &maps.hi_ep[cur], &sm.eload[ew], col0, row0, t.b);
-                                tma_load_3d(sm.stage[ew][1], &maps.lo_ep, &sm.eload[ew], col0, row0, t.b);
-                            }
+                            mbar_arrive_expect_tx(&sm.eload[ew], in0 && in1 ? 8192 : 4096);
+                            if (in0)
+                                tma_load_3d(sm.stage[ew][0], update ? &maps.hi_ep : &maps.sq_ep, &sm.eload[ew], col0, row0,
+                                            (update ? cur : t.sym->u) * g.mats + t.b);
+                            if (in1)
+                                tma_load_3d(sm.stage[ew][1], update ? &maps.lo_ep : &maps.sq_ep, &sm.eload[ew], col0, row0,
+                                            (update ? 0 : t.sym->v) * g.mats + t.b);
                         }
                     }
                 }
@@ -342,7 +376,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                     if (!mbar_wait(&sm.tfull[buf], (ti >> 1) & 1, kOrthoWaitNs)) { fail(); ok = false; break; }
                     tc_fence_after();
                 }
-                if (t.prod != 0) {
+                if (in0 || in1) {
                     if (!mbar_wait(&sm.eload[ew], loads & 1, kOrthoWaitNs)) { fail(); ok = false; break; }
                     ++loads;
                 }
@@ -362,11 +396,31 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                 // 16-byte piece p (8 columns) of row `lane` sits at p ^ (lane & 7) (128-byte swizzle); four at a time,
                 // all of a turn's reads before its writes, which are in place
                 auto at = [&](int p) { return static_cast<uint32_t>(lane * 128 + ((p ^ (lane & 7)) << 4)); };
+                if (!update) {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) v[i >> 5][i & 31] *= cxy;
+                    if (in1) {
+                        // the second addend first and whole: the transposed box goes over it
+#pragma unroll
+                        for (int p = 0; p < 8; ++p) {
+                            const uint4 r = ld_shared_v4(st1 + at(p));
+                            const uint32_t rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 f = unpack_half2(rr[i]);
+                                float (&x)[32] = v[p >> 2];
+                                x[(p & 3) * 8 + 2 * i] = fmaf(cv, f.x, x[(p & 3) * 8 + 2 * i]);
+                                x[(p & 3) * 8 + 2 * i + 1] = fmaf(cv, f.y, x[(p & 3) * 8 + 2 * i + 1]);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
 #pragma unroll
                 for (int hp = 0; hp < 2; ++hp) {
                     float (&x)[32] = v[hp];
                     uint32_t o[4][4];
-                    if (t.prod == 2) {
+                    if (update) {
                         uint4 u[4], r[4];
 #pragma unroll
                         for (int p = 0; p < 4; ++p) { u[p] = ld_shared_v4(st0 + at(hp * 4 + p)); r[p] = ld_shared_v4(st1 + at(hp * 4 + p)); }
@@ -378,7 +432,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                                 const float2 h = unpack_half2(uu[i]), lo = unpack_half2(rr[i]);
                                 float& x0 = x[p * 8 + 2 * i];
                                 float& x1 = x[p * 8 + 2 * i + 1];
-                                const float2 y = __ffma2_rn(make_float2(g.a, g.a), __fadd2_rn(h, lo),
+                                const float2 y = __ffma2_rn(make_float2(ca, ca), __fadd2_rn(h, lo),
                                                             __fmul2_rn(make_float2(inv, inv), make_float2(x0, x1)));
                                 x0 = y.x;
                                 x1 = y.y;
@@ -403,7 +457,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                             }
                         }
                     } else {
-                        if (t.prod == 1) {
+                        if (in0) {
                             uint4 u[4];
 #pragma unroll
                             for (int p = 0; p < 4; ++p) u[p] = ld_shared_v4(st0 + at(hp * 4 + p));
@@ -413,16 +467,14 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
 #pragma unroll
                                 for (int i = 0; i < 4; ++i) {
                                     const float2 f = unpack_half2(uu[i]);
-                                    o[p][i] = pack_half2(fmaf(g.b, f.x, quad * x[p * 8 + 2 * i]),
-                                                         fmaf(g.b, f.y, quad * x[p * 8 + 2 * i + 1]));
+                                    o[p][i] = pack_half2(fmaf(cu, f.x, x[p * 8 + 2 * i]), fmaf(cu, f.y, x[p * 8 + 2 * i + 1]));
                                 }
                             }
                         } else {
 #pragma unroll
                             for (int p = 0; p < 4; ++p)
 #pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    o[p][i] = pack_half2(x[p * 8 + 2 * i] * g.gram_scale, x[p * 8 + 2 * i + 1] * g.gram_scale);
+                                for (int i = 0; i < 4; ++i) o[p][i] = pack_half2(x[p * 8 + 2 * i], x[p * 8 + 2 * i + 1]);
                         }
                         if (mirror) {
                             // the transposed box: row j (a column here) of 32 values, 64-byte swizzle
@@ -466,10 +518,10 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                     __syncwarp();
                     if (lane == 0) {
                         if (row0 < rows && col0 < cols) {
-                            const CUtensorMap* m = t.prod == 0 ? &maps.p_ep : t.prod == 1 ? &maps.q_ep : &maps.hi_ep[cur ^ 1];
-                            tma_store_3d(m, sm.stage[ew][0], col0, row0, t.b);
-                            if (t.prod == 2) tma_store_3d(&maps.lo_ep, sm.stage[ew][1], col0, row0, t.b);
-                            if (mirror) tma_store_3d(t.prod == 0 ? &maps.p_tr : &maps.q_tr, sm.stage[ew][1], row0, col0, t.b);
+                            const int z = (update ? cur ^ 1 : t.kind == kGram ? 0 : t.sym->out) * g.mats + t.b;
+                            tma_store_3d(update ? &maps.hi_ep : &maps.sq_ep, sm.stage[ew][0], col0, row0, z);
+                            if (update) tma_store_3d(&maps.lo_ep, sm.stage[ew][1], col0, row0, t.b);
+                            if (mirror) tma_store_3d(&maps.sq_tr, sm.stage[ew][1], row0, col0, z);
                         }
                         bulk_commit();
                     }
@@ -642,11 +694,15 @@ int wave_of(int mats, int M, int N, int interleaved) {
     return w;
 }
 
+// The first two steps at once. Measured on a B200 (us, step by step / merged): two of 2048 x 7168 910 / 815, four of
+// 4096 x 2048 1069 / 984, one of 2048 x 4096 400 / 396, four of 1024 x 2048 251 / 257: below 1024 the one product more
+// in a row costs what the flops save.
+bool merges(int M, int N) { return std::min(M, N) >= 1024 && 2 * std::max(M, N) >= 3 * std::min(M, N); }
+
 struct OrthoWs {
-    uint16_t* hi[2];
+    uint16_t* hi;        // two buffers of X's first parts
     uint16_t* lo;
-    uint16_t* p;
-    uint16_t* q;
+    uint16_t* sq;        // the slots of s x s matrices
     double* part;
     unsigned* done;
     size_t total;
@@ -662,10 +718,9 @@ OrthoWs carve_ortho(int wave, int M, int N, void* base) {
         off += (bytes + 255) / 256 * 256;
         return r;
     };
-    for (auto& h : w.hi) h = reinterpret_cast<uint16_t*>(take(2 * wave * M * ldx));
+    w.hi = reinterpret_cast<uint16_t*>(take(2 * 2 * wave * M * ldx));
     w.lo = reinterpret_cast<uint16_t*>(take(2 * wave * M * ldx));
-    w.p = reinterpret_cast<uint16_t*>(take(2 * wave * s * lds));
-    w.q = reinterpret_cast<uint16_t*>(take(2 * wave * s * lds));
+    w.sq = reinterpret_cast<uint16_t*>(take(2 * (merges(M, N) ? kSlots : 2) * wave * s * lds));
     w.part = reinterpret_cast<double*>(take(8ull * wave * kNormBlocks));
     w.done = reinterpret_cast<unsigned*>(take(4ull * wave * kDoneStride));
     w.total = off;
@@ -696,6 +751,9 @@ moe_status_t check_ortho(int batch, int M, int N, int interleaved) {
 // Whether every X and B of the iteration stays inside what fp16 holds: bounds the largest singular value after
 // each step from that before it (|a x + b x^3 + c x^5| over [0, r] has its maximum at r or where the derivative
 // is zero), and |b x^2 + c x^4| likewise.
+// Two steps at once stay inside with them: with r the bound after the first, the odd quintic p is at most r on
+// [0, 1] and 8 on [0, r], so by Bernstein's inequality |p(x) / x| is at most 5 pi / 2 r and 5 pi / 2 8 / r there and
+// a^2 <= 5 r 40 / r; Q = (a I + B_2)(a I + B_1) - a^2 I is then below 700, times 64 below 2^16 - 2^14.
 bool coefficients_ok(int steps, float a, float b, float c) {
     if (!std::isfinite(a) || !std::isfinite(b) || !std::isfinite(c)) return false;
     const double A = a, B = b, C = c;
@@ -742,7 +800,7 @@ cudaError_t launch_prepare(const void* G, int mats, const OrthoArgs& g, const Or
                                              G, g.M, g.N, g.interleaved, w.part, w.done);
     if (err != cudaSuccess) return err;
     return launch_dependent(vec ? ortho_convert_kernel<F32, true> : ortho_convert_kernel<F32, false>, grid, block, 0, s, G, g.M,
-                            g.N, ldx, g.interleaved, w.part, eps, xscale, w.hi[0], w.lo);
+                            g.N, ldx, g.interleaved, w.part, eps, xscale, w.hi, w.lo);
 }
 
 template <bool PAIR>
@@ -823,11 +881,20 @@ moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const v
         g.M = M;
         g.N = N;
         g.mats = std::min(wave, mats - m0);
-        g.steps = steps;
         g.interleaved = interleaved;
-        g.a = a;
-        g.b = b;
-        g.c = c;
+        // slots: 0 A, 1 Q; of two steps in one also 2 B_1, 3 B_1 A, 4 A_2, 5 B_2
+        const float f = 1.0f / kPScale;
+        const bool two = steps >= 2 && merges(M, N);
+        g.sym = {0, 0, 0, -1, 1, c * f, b, 0.0f};
+        g.sym0[0] = two ? OrthoSym{0, 0, 0, -1, 2, c * f, b, 0.0f} : g.sym;
+        g.sym0[1] = {2, 0, -1, -1, 3, f, 0.0f, 0.0f};
+        g.sym0[2] = {2, 3, 0, 3, 4, f, a * a, 2.0f * a};
+        g.sym0[3] = {4, 4, 4, -1, 5, c * f, b, 0.0f};
+        g.sym0[4] = {5, 2, 2, 5, 1, f, a, a};
+        g.nsym0 = two ? kMostSym : 1;
+        g.groups = two ? steps - 1 : steps;
+        g.ca0 = two ? a * a : a;
+        g.ca = a;
         g.out_scale = static_cast<float>(scale / xscale);
         g.gram_scale = static_cast<float>(kPScale / (xscale * xscale));
         const size_t first = static_cast<size_t>(m0) * M * N;
@@ -836,19 +903,13 @@ moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const v
         g.status = status;
         const void* gw = static_cast<const uint8_t*>(G) + first * size;
         OrthoMaps maps;
-        bool ok = true;
-        for (int i = 0; i < 2; ++i) {
-            ok = ok && make_half_map(&maps.hi_op[i], w.hi[i], g.mats, M, N, 64, 64);
-            ok = ok && make_half_map(&maps.hi_ep[i], w.hi[i], g.mats, M, N, 64, 32);
-        }
-        ok = ok && make_half_map(&maps.lo_ep, w.lo, g.mats, M, N, 64, 32);
-        ok = ok && make_half_map(&maps.p_op, w.p, g.mats, side, side, 64, 64);
-        ok = ok && make_half_map(&maps.p_ep, w.p, g.mats, side, side, 64, 32);
-        ok = ok && make_half_map(&maps.p_tr, w.p, g.mats, side, side, 32, 64);
-        ok = ok && make_half_map(&maps.q_op, w.q, g.mats, side, side, 64, 64);
-        ok = ok && make_half_map(&maps.q_ep, w.q, g.mats, side, side, 64, 32);
-        ok = ok && make_half_map(&maps.q_tr, w.q, g.mats, side, side, 32, 64);
-        if (!ok) return MOE_ERR_CUDA;
+        const int slots = merges(M, N) ? kSlots : 2;
+        if (!make_half_map(&maps.hi_op, w.hi, 2 * g.mats, M, N, 64, 64) || !make_half_map(&maps.hi_ep, w.hi, 2 * g.mats, M, N, 64, 32) ||
+            !make_half_map(&maps.lo_ep, w.lo, g.mats, M, N, 64, 32) ||
+            !make_half_map(&maps.sq_op, w.sq, slots * g.mats, side, side, 64, 64) ||
+            !make_half_map(&maps.sq_ep, w.sq, slots * g.mats, side, side, 64, 32) ||
+            !make_half_map(&maps.sq_tr, w.sq, slots * g.mats, side, side, 32, 64))
+            return MOE_ERR_CUDA;
         cudaError_t err = g_type == MOE_TYPE_FP32 ? launch_prepare<true>(gw, g.mats, g, w, eps, xscale, s)
                                                   : launch_prepare<false>(gw, g.mats, g, w, eps, xscale, s);
         if (err == cudaSuccess)

@@ -70,6 +70,26 @@ def test_interleaved_pairs(M, N):
             close(ref.split(O[i])[j], pairs[i, j].to(torch.bfloat16), scale=0.5)
 
 
+@pytest.mark.parametrize("batch,M,N,inter", [(1, 1024, 1536, False), (2, 2100, 1030, False), (3, 1024, 2048, True), (1, 1153, 1801, False),
+                                             (1, 1200, 1400, False), (6, 1500, 1000, False)])
+@pytest.mark.parametrize("kind", ["noise", "low_rank", "decay", "spikes"])
+def test_large_matrices(batch, M, N, inter, kind):
+    # the sizes that take their first two steps at once, and some beside them; the iteration in 64 bits on the GPU
+    pairs = torch.stack([ortho_matrix(M, N, kind, i) for i in range(batch * (2 if inter else 1))]).cuda()
+    G = torch.stack([ref.interleave(p) for p in pairs.view(batch, 2, M, N)]) if inter else pairs
+    O = done(run(G, batch, M, N, inter))
+    O = torch.cat([ref.split(o) for o in O]) if inter else O
+    for i in range(pairs.shape[0]):
+        assert ref.rel_norm(O[i], ref.orthogonalise(pairs[i])) <= 2.0 ** -8 + 2.0 ** -8
+
+
+@pytest.mark.parametrize("steps,coef", [(1, ref.ORTHO), (2, ref.ORTHO), (3, (1.875, -1.25, 0.375)), (2, (2.0, -1.5, 0.5))])
+def test_large_matrices_with_other_steps_and_coefficients(steps, coef):
+    G = ortho_matrix(1024, 1600, "noise", 8).cuda()[None].contiguous()
+    O = done(run(G, 1, 1024, 1600, steps=steps, coef=coef))
+    assert ref.rel_norm(O[0], ref.orthogonalise(G[0], steps, coef)) <= 2.0 ** -8 + 2.0 ** -7
+
+
 def test_a_batch_of_more_than_one_wave():
     # waves of a large batch use the workspace in turn: every matrix as if alone
     M, N, batch = 520, 520, 30

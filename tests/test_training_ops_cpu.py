@@ -78,8 +78,21 @@ def test_orthogonalisation_roundings_stay_below_bf16_rounding(M, N, kind):
     assert ref.rel_norm(ref.orthogonalise_model(G), ref.orthogonalise(G)) <= 2.0 ** -7
 
 
+@pytest.mark.parametrize("M,N", [(128, 256), (384, 1024), (700, 300)])
+@pytest.mark.parametrize("kind", ["noise", "low_rank", "decay", "spikes"])
+def test_the_first_two_steps_at_once_add_little(M, N, kind):
+    G = ortho_matrix(M, N, kind, 5)
+    exact = ref.orthogonalise(G)
+    plain, merged = (ref.rel_norm(ref.orthogonalise_model(G, merged=m), exact) for m in (False, True))
+    assert merged <= 2.0 ** -8 and merged <= 1.5 * plain + 2.0 ** -11
+
+
 def ortho_matrix(M, N, kind, seed):
     g = torch.Generator().manual_seed(seed + 1000 * M + N)
+    if kind == "spikes":
+        u = torch.linalg.qr(torch.randn(M, 4, generator=g))[0]
+        v = torch.linalg.qr(torch.randn(N, 4, generator=g))[0]
+        return 30 * u @ v.t() + torch.randn(M, N, generator=g) / (M ** 0.5 + N ** 0.5)
     if kind == "noise":
         return torch.randn(M, N, generator=g)
     r = min(M, N, 8) if kind == "low_rank" else min(M, N)

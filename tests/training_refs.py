@@ -72,9 +72,10 @@ def orthogonalise(G, steps=5, coef=ORTHO, eps=1e-7):
     return X.t() if tall else X
 
 
-def orthogonalise_model(G, steps=5, coef=ORTHO, eps=1e-7):
+def orthogonalise_model(G, steps=5, coef=ORTHO, eps=1e-7, merged=False):
     """The same with the kernel's roundings, sums in 64 bits: products of fp16 X, 64 A and 64 B; X carried as two
-    fp16 values that both enter a X; X times a power of two near the square root of the longer side."""
+    fp16 values that both enter a X; X times a power of two near the square root of the longer side. merged: the
+    first two steps at once, as large matrices take them."""
     a, b, c = coef
     h = lambda t: t.to(torch.float16).double()
     X = G.double()
@@ -82,7 +83,15 @@ def orthogonalise_model(G, steps=5, coef=ORTHO, eps=1e-7):
     X = X.t() if tall else X
     S = 2.0 ** np.floor(0.5 * np.log2(max(X.shape)) + 0.5)
     X = X / (X.norm() + eps) * S
-    for _ in range(steps):
+    if merged:
+        hi = h(X)
+        P = h(hi @ hi.t() * (64 / S ** 2))
+        B1 = h(b * P + c / 64 * (P @ P))
+        D = h(B1 @ P / 64)
+        A2 = h(a * a * P + 2 * a * D + B1 @ D / 64)
+        B2 = h(b * A2 + c / 64 * (A2 @ A2))
+        X = a * a * (hi + h(X - hi)) + h(a * (B1 + B2) + B2 @ B1 / 64) @ hi / 64
+    for _ in range(steps - 2 if merged else steps):
         hi = h(X)
         P = h(hi @ hi.t() * (64 / S ** 2))
         Q = h(b * P + c / 64 * (P @ P))
