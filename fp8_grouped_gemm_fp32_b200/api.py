@@ -278,20 +278,23 @@ def moe_backward(cfg, x, Wg, W13, S13, W13T, S13T, W2T, S2T, topk_idx, topk_w, s
 
 # ---------------------------------------------------------------- balance loss, the router's gradient, updates
 def _args(*tensors):
-    """The tensors' pointers (None and empty ones: null), all checked to be contiguous and on the current device,
-    where the library launches whatever device a pointer is of."""
-    out, dev = [], torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -1
+    """The tensors' pointers (None: null), all checked to be contiguous and on the current device, where the library
+    launches whatever device a pointer is of."""
+    out, dev = [], None
     for t in tensors:
-        ptr = None
-        if t is not None:
-            ptr = t.data_ptr() or None
-            if ptr and not t.is_cuda:
+        if t is None:
+            out.append(None)
+            continue
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
                 raise ValueError("moe_fp8 entry points take CUDA tensors")
-            if ptr and t.get_device() != dev:
-                raise ValueError(f"a tensor of cuda:{t.get_device()} in a call on the current device cuda:{dev}")
-            if not t.is_contiguous():
-                raise ValueError("moe_fp8 entry points take contiguous tensors")
-        out.append(ptr)
+            dev = torch._C._cuda_getDevice()
+            if d != dev:
+                raise ValueError(f"a tensor of cuda:{d} in a call on the current device cuda:{dev}")
+        if not t.is_contiguous():
+            raise ValueError("moe_fp8 entry points take contiguous tensors")
+        out.append(t.data_ptr())
     return out
 
 

@@ -682,6 +682,323 @@ ortho_convert_kernel(const void* __restrict__ G, int M, int N, int ldx, int inte
     }
 }
 
+// ---------------------------------------------------------------- a shorter side of at most 128
+// Here a step's products are small and the way between them is the time, so one launch does everything and only X
+// crosses between CTAs, once a step. Each CTA owns 128 columns of Y (X, or X^T where G is tall: s rows, l columns), in
+// fp32 registers, with their fp16 values as an MMA operand in shared memory; it computes A over all of Y itself (all
+// CTAs of a matrix the same bits: one order of K blocks), then B, in shared memory too, and its columns of the update.
+// The first exchange is the partial sums of |G|^2. Measured on a B200 (us, against the kernel above with its two
+// preparing launches): 64 x 64 28 / 64, 148 of them 29 / 130, 8 of 128 x 256 49 / 78, 2 of 100 x 1000 70 / 101,
+// 128 x 4096 153 / 167, 64 of 128 x 512 116 / 134. A step is 5500 cycles and an exchange 5000 to 7000 more.
+constexpr int kNStages = 5;
+
+struct SmemN {
+    uint8_t ring[kNStages][kOOper];      // K blocks of Y: 128 rows x 64 columns
+    uint8_t y[2][kOOper];                // this CTA's columns, two blocks of 64
+    uint8_t p[2][kOOper];                // 64 A
+    uint8_t q[2][kOOper];                // 64 B
+    uint64_t full[kNStages], empty[kNStages];
+    uint64_t acc[3];                     // A, A^2 and B Y are in tensor memory
+    uint64_t norm, p_ready, q_ready, y_ready, y_stored;
+    double red[kOEpi];
+    double inv;
+    uint32_t tmem_base;
+    volatile int abort_flag;
+};
+
+struct NarrowArgs {
+    const void* G;
+    int M, N, tiles;                     // tiles: CTAs of a matrix
+    int interleaved, steps;
+    float a, b, c;
+    double eps, xscale;
+    float out_scale, gram_scale;
+    uint16_t* O;
+    double* part;                        // [mats][tiles]
+    unsigned* done;                      // [mats][kDoneStride], zero at the start
+    int* status;
+};
+
+template <bool F32>
+__global__ void __launch_bounds__(kOThreads, 1)
+ortho_narrow_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_constant__ NarrowArgs g) {
+    extern __shared__ uint8_t smem_raw[];
+    SmemN& sm = *reinterpret_cast<SmemN*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int m = blockIdx.x / g.tiles, own = blockIdx.x % g.tiles, mats = gridDim.x / g.tiles;
+    const bool tall = g.M > g.N;
+    const int s = min(g.M, g.N), l = max(g.M, g.N);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kNStages; ++i) { mbar_init(&sm.full[i], 1); mbar_init(&sm.empty[i], 1); }
+        for (int i = 0; i < 3; ++i) mbar_init(&sm.acc[i], 1);
+        mbar_init(&sm.norm, 1);
+        mbar_init(&sm.p_ready, kOEpi);
+        mbar_init(&sm.q_ready, kOEpi);
+        mbar_init(&sm.y_ready, kOEpi);
+        mbar_init(&sm.y_stored, kOEpi);
+        sm.abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) { tmem_alloc(&sm.tmem_base, 512); tmem_relinquish(); }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    unsigned* const done = g.done + m * kDoneStride;
+    auto fail = [&]() { set_status(g.status, kStatusTimeout); sm.abort_flag = 1; };
+    auto wait_for = [&](unsigned need) -> bool {
+        const uint64_t t0 = globaltimer_ns();
+        while (load_acquire_gpu(done) < need)
+            if (sm.abort_flag || globaltimer_ns() - t0 > kOrthoWaitNs) return false;
+        return true;
+    };
+
+    if (warp == 0) {
+        // ---------------- producer: the other CTAs' columns of Y
+        if (lane == 0 && g.tiles > 1) {
+            uint32_t it = 0;
+            bool ok = true;
+            for (int step = 0; ok && step < g.steps; ++step) {
+                // counted once for the norm and once for every Y before this step's
+                if (!wait_for(static_cast<unsigned>(step + 2) * g.tiles)) { fail(); break; }
+                fence_proxy_async();
+                for (int kb = 0; kb < 2 * g.tiles; ++kb) {
+                    if (kb >> 1 == own) continue;
+                    const int st = it % kNStages;
+                    if (!mbar_wait(&sm.empty[st], ((it / kNStages) & 1) ^ 1, kOrthoWaitNs)) { fail(); ok = false; break; }
+                    mbar_arrive_expect_tx(&sm.full[st], kOOper);
+                    tma_load_3d(sm.ring[st], &tm_y, &sm.full[st], kb * 64, 0, (step & 1) * mats + m);
+                    ++it;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ---------------- MMA issuer
+        if (lane == 0) {
+            uint32_t it = 0;
+            const uint32_t kk_desc = f16_idesc(128, 128, false, false, false), km_desc = f16_idesc(128, 128, false, false, true);
+            bool ok = true;
+            for (int step = 0; ok && step < g.steps && !sm.abort_flag; ++step) {
+                if (!mbar_wait(&sm.y_ready, step & 1, kOrthoWaitNs)) { fail(); break; }
+                tc_fence_after();
+                for (int kb = 0; kb < 2 * g.tiles; ++kb) {
+                    const bool mine = kb >> 1 == own;
+                    const int st = it % kNStages;
+                    if (!mine && !mbar_wait(&sm.full[st], (it / kNStages) & 1, kOrthoWaitNs)) { fail(); ok = false; break; }
+                    tc_fence_after();
+                    const uint64_t d = sw128_kmajor_desc(smem_u32(mine ? sm.y[kb & 1] : sm.ring[st]));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) umma_f16(tmem, d + kk * 2, d + kk * 2, kk_desc, kb + kk > 0);
+                    if (!mine) {
+                        umma_commit(&sm.empty[st]);
+                        ++it;
+                    }
+                }
+                if (!ok) break;
+                umma_commit(&sm.acc[0]);
+                if (!mbar_wait(&sm.p_ready, step & 1, kOrthoWaitNs)) { fail(); break; }
+                tc_fence_after();
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    const uint64_t d = sw128_kmajor_desc(smem_u32(sm.p[kb]));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) umma_f16(tmem + 128, d + kk * 2, d + kk * 2, kk_desc, kb + kk > 0);
+                }
+                umma_commit(&sm.acc[1]);
+                if (!mbar_wait(&sm.q_ready, step & 1, kOrthoWaitNs)) { fail(); break; }
+                tc_fence_after();
+                // B (K-major) times this CTA's Y (MN-major: 64-column blocks of 128 rows)
+                const uint64_t dy = sw128_mnmajor_desc(smem_u32(sm.y[0]), kOOper);
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+                    const uint64_t d = sw128_kmajor_desc(smem_u32(sm.q[kb]));
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) umma_f16(tmem + 256, d + kk * 2, dy + (kb * 4 + kk) * 128, km_desc, kb + kk > 0);
+                }
+                umma_commit(&sm.acc[2]);
+            }
+        }
+    } else if (warp >= 4) {
+        // ---------------- the rest: a thread holds row `row`, 64 columns (of Y: col0 ..)
+        const int ew = warp - 4, q = warp & 3, half = ew >> 2;
+        const int row = q * 32 + lane, col0 = own * 128 + half * 64;
+        const uint32_t lanes = static_cast<uint32_t>(q * 32) << 16;
+        auto at = [&](int p) { return static_cast<uint32_t>(row * 128 + ((p ^ (row & 7)) << 4)); };
+        auto put = [&](uint8_t (*blocks)[kOOper], const uint32_t (&o)[32]) {
+            const uint32_t base = smem_u32(blocks[half]);
+#pragma unroll
+            for (int p = 0; p < 8; ++p) st_shared_v4(base + at(p), o[4 * p], o[4 * p + 1], o[4 * p + 2], o[4 * p + 3]);
+        };
+        auto arrive = [&](uint64_t* bar) {
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        // Memory is read and written along the caller's rows, 64 accesses of a lane in flight: those are the lanes where
+        // G is tall, else this warp's 32 x 64 values go through shared memory, column c of row r at r * 64 + (c ^ r).
+        // The 32 rows of a warp (the 64 of its columns, where tall) lie one after another in the caller's array.
+        float* const turn = reinterpret_cast<float*>(sm.p[0]) + ew * 2048;
+        const int64_t base = tall ? user_row(m, col0, g.M, g.interleaved) * g.N + row
+                                  : user_row(m, q * 32, g.M, g.interleaved) * g.N + col0 + lane;
+        auto load = [&](int64_t e) {
+            return F32 ? static_cast<const float*>(g.G)[e] : bf16_bits_to_f32(static_cast<const uint16_t*>(g.G)[e]);
+        };
+        float x[64];
+        bool ok = true;
+        // Y's tile and the norm
+        if (tall) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] = row < s && col0 + i < l ? load(base + static_cast<int64_t>(i) * g.N) : 0.0f;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 64; ++i) {
+                const int r = i >> 1, c = 32 * (i & 1);
+                x[i] = q * 32 + r < s && col0 + c + lane < l ? load(base + static_cast<int64_t>(r) * g.N + c) : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 64; ++i) turn[(i >> 1) * 64 + ((32 * (i & 1) + lane) ^ (i >> 1))] = x[i];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] = turn[lane * 64 + (i ^ lane)];
+        }
+        double sq[4] = {};
+#pragma unroll
+        for (int i = 0; i < 64; ++i) sq[i & 3] = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), sq[i & 3]);
+        double ss = (sq[0] + sq[1]) + (sq[2] + sq[3]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        int good = 1;
+        if (lane == 0) {
+            sm.red[ew] = ss;
+            mbar_arrive(&sm.y_stored);
+            if (ew == 0) {
+                good = mbar_wait(&sm.y_stored, 0, kOrthoWaitNs);
+                double t = 0.0;
+                for (int i = 0; i < kOEpi; ++i) t += sm.red[i];
+                if (good && g.tiles > 1) {
+                    g.part[static_cast<int64_t>(m) * g.tiles + own] = t;
+                    add_release_gpu(done, 1);
+                    good = wait_for(g.tiles);
+                    t = 0.0;
+                    for (int i = 0; good && i < g.tiles; ++i) t += __ldcg(g.part + static_cast<int64_t>(m) * g.tiles + i);
+                }
+                sm.inv = g.xscale / (sqrt(t) + g.eps);
+                if (good) mbar_arrive(&sm.norm);
+            }
+        }
+        good = __shfl_sync(0xffffffffu, good, 0);
+        if (!good || !mbar_wait(&sm.norm, 0, kOrthoWaitNs)) { fail(); ok = false; }
+        const double inv = sm.inv;
+        if (inv > 1e-30 && inv < 1e30) {
+            const float f = static_cast<float>(inv);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] *= f;
+        } else {                                         // the inverse of such a norm leaves fp32, or is not a number
+#pragma unroll
+            for (int i = 0; i < 64; ++i) x[i] = static_cast<float>(x[i] * inv);
+        }
+        // this CTA's Y: operand, and (other CTAs' operand) to memory
+        auto publish = [&](int buf, uint32_t phase) -> bool {
+            uint32_t o[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = pack_half2(x[2 * i], x[2 * i + 1]);
+            put(sm.y, o);
+            arrive(&sm.y_ready);
+            if (g.tiles == 1) return true;
+            int fine = 1;
+            if (lane == 0) {
+                mbar_arrive(&sm.y_stored);               // (behind the fence: the blocks are whole when it completes)
+                if (ew == 0) {
+                    fine = mbar_wait(&sm.y_stored, phase, kOrthoWaitNs);
+                    if (fine) {
+                        for (int i = 0; i < 2; ++i)
+                            if (own * 128 + 64 * i < l) tma_store_3d(&tm_y, sm.y[i], own * 128 + 64 * i, 0, buf * mats + m);
+                        bulk_commit();
+                        bulk_wait_all();
+                        add_release_gpu(done, 1);
+                    }
+                }
+            }
+            return __shfl_sync(0xffffffffu, fine, 0) != 0;
+        };
+        if (ok && !publish(0, 1)) { fail(); ok = false; }
+        const float quad = g.c * (1.0f / kPScale), unit = 1.0f / kPScale;
+        for (int step = 0; ok && step < g.steps; ++step) {
+            if (sm.abort_flag) break;
+            uint32_t o[32];
+            if (!mbar_wait(&sm.acc[0], step & 1, kOrthoWaitNs)) { fail(); break; }
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[32];
+                tmem_ld32(tmem + lanes + half * 64 + 32 * h, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[16 * h + i] = pack_half2(v[2 * i] * g.gram_scale, v[2 * i + 1] * g.gram_scale);
+            }
+            put(sm.p, o);
+            arrive(&sm.p_ready);
+            if (!mbar_wait(&sm.acc[1], step & 1, kOrthoWaitNs)) { fail(); break; }
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[32];
+                tmem_ld32(tmem + lanes + 128 + half * 64 + 32 * h, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 f = unpack_half2(o[16 * h + i]);
+                    o[16 * h + i] = pack_half2(fmaf(g.b, f.x, quad * v[2 * i]), fmaf(g.b, f.y, quad * v[2 * i + 1]));
+                }
+            }
+            put(sm.q, o);
+            arrive(&sm.q_ready);
+            if (!mbar_wait(&sm.acc[2], step & 1, kOrthoWaitNs)) { fail(); break; }
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float v[32];
+                tmem_ld32(tmem + lanes + 256 + half * 64 + 32 * h, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[32 * h + i] = fmaf(g.a, x[32 * h + i], unit * v[i]);
+            }
+            if (step + 1 < g.steps && !publish((step + 1) & 1, step & 1)) { fail(); break; }
+        }
+        if (ok && !sm.abort_flag) {
+            auto bits = [&](float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(g.out_scale * f)); };
+            if (tall) {
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    if (row < s && col0 + i < l) g.O[base + static_cast<int64_t>(i) * g.N] = bits(x[i]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 64; ++i) turn[lane * 64 + (i ^ lane)] = x[i];
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 64; ++i) {
+                    const int r = i >> 1, c = 32 * (i & 1);
+                    if (q * 32 + r < s && col0 + c + lane < l)
+                        g.O[base + static_cast<int64_t>(r) * g.N + c] = bits(turn[r * 64 + ((c + lane) ^ r)]);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (sm.abort_flag) {
+        const uint64_t t0 = globaltimer_ns();
+        while (globaltimer_ns() - t0 < 200000) __nanosleep(1000);   // copies and MMAs in flight land
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
 // ---------------------------------------------------------------- workspace and launches
 // A wave holds enough matrices to give every CTA pair a tile of the symmetric products, twice over, and never
 // fewer than two (one fills the other's waits); a batch is cut into equal waves that use the workspace in turn.
@@ -790,6 +1107,38 @@ int tiles_of(int M, int N) {
 // 1570 / 1061.
 bool use_pairs(int mats, int M, int N) { return static_cast<int64_t>(mats) * tiles_of<true>(M, N) >= 56; }
 
+// The narrow kernel's CTAs all compute A, so a matrix of many of them only where all matrices run at once.
+int narrow_tiles(int M, int N) { return (std::max(M, N) + 127) / 128; }
+bool use_narrow(int mats, int M, int N) {
+    const int t = narrow_tiles(M, N);
+    return std::min(M, N) <= 128 && (t <= 4 || static_cast<int64_t>(mats) * t <= 148);
+}
+
+struct NarrowWs {
+    uint16_t* y;         // two buffers of the wave's Y
+    double* part;
+    unsigned* done;
+    size_t total;
+};
+constexpr int kNarrowSms = 148;
+NarrowWs carve_narrow(int mats, int M, int N, void* base) {
+    NarrowWs w;
+    const int t = narrow_tiles(M, N);
+    const size_t wave = std::min(mats, kNarrowSms / t), s = std::min(M, N), ld = (std::max(M, N) + 7) / 8 * 8;
+    uint8_t* p = static_cast<uint8_t*>(base);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        uint8_t* r = p ? p + off : nullptr;
+        off += (bytes + 255) / 256 * 256;
+        return r;
+    };
+    w.y = reinterpret_cast<uint16_t*>(take(2 * 2 * wave * s * ld));
+    w.part = reinterpret_cast<double*>(take(8 * wave * t));
+    w.done = reinterpret_cast<unsigned*>(take(4 * wave * kDoneStride));
+    w.total = off;
+    return w;
+}
+
 template <bool F32>
 cudaError_t launch_prepare(const void* G, int mats, const OrthoArgs& g, const OrthoWs& w, double eps, double xscale,
                            cudaStream_t s) {
@@ -843,6 +1192,40 @@ cudaError_t launch_steps(const OrthoMaps& maps, const OrthoArgs& g, int num_sms,
     return cudaLaunchKernelEx(&cfg, kern, maps, g);
 }
 
+template <bool F32>
+cudaError_t launch_narrow(NarrowArgs g, const NarrowWs& w, int mats, int num_sms, cudaStream_t s) {
+    const size_t smem = sizeof(SmemN) + 1024;
+    cudaError_t err = cudaFuncSetAttribute(ortho_narrow_kernel<F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (err != cudaSuccess) return err;
+    // every wave at once on the GPU; of interleaved pairs both
+    int wave = std::min(mats, std::min(num_sms, kNarrowSms) / g.tiles);
+    if (g.interleaved) wave &= ~1;
+    if (wave <= 0) return cudaErrorInvalidConfiguration;
+    const uint8_t* G = static_cast<const uint8_t*>(g.G);
+    uint16_t* const O = g.O;
+    for (int m0 = 0; m0 < mats; m0 += wave) {
+        const int n = std::min(wave, mats - m0);
+        const size_t first = static_cast<size_t>(m0) * g.M * g.N;
+        CUtensorMap map;
+        if (!make_half_map(&map, w.y, 2 * n, std::min(g.M, g.N), std::max(g.M, g.N), 64, 128)) return cudaErrorInvalidValue;
+        g.G = G + first * (F32 ? 4 : 2);
+        g.O = O + first;
+        if (g.tiles > 1 && (err = cudaMemsetAsync(w.done, 0, 4ull * n * kDoneStride, s)) != cudaSuccess) return err;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeCooperative;      // the CTAs of a matrix wait on one another
+        attr[0].val.cooperative = 1;
+        cfg.gridDim = dim3(n * g.tiles);
+        cfg.blockDim = dim3(kOThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if ((err = cudaLaunchKernelEx(&cfg, ortho_narrow_kernel<F32>, map, g)) != cudaSuccess) return err;
+    }
+    return cudaSuccess;
+}
+
 bool ptr_ok(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
@@ -854,7 +1237,9 @@ extern "C" {
 
 size_t moe_orthogonalise_workspace_size(int batch, int M, int N, int interleaved) {
     if (check_ortho(batch, M, N, interleaved) != MOE_OK || batch == 0) return 0;
-    return carve_ortho(wave_of(batch * (interleaved ? 2 : 1), M, N, interleaved), M, N, nullptr).total;
+    const int mats = batch * (interleaved ? 2 : 1);
+    if (use_narrow(mats, M, N)) return carve_narrow(mats, M, N, nullptr).total;
+    return carve_ortho(wave_of(mats, M, N, interleaved), M, N, nullptr).total;
 }
 
 moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const void* G, int g_type, int steps, float a,
@@ -868,14 +1253,39 @@ moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const v
     if (batch == 0) return MOE_OK;
     if (!ptr_ok(G) || !ptr_ok(O) || !ptr_ok(ws) || (reinterpret_cast<uintptr_t>(ws) & 255)) return MOE_ERR_INVALID_ARG;
     const int mats = batch * (interleaved ? 2 : 1), wave = wave_of(mats, M, N, interleaved);
+    const bool narrow = use_narrow(mats, M, N);
     const OrthoWs w = carve_ortho(wave, M, N, ws);
-    if (ws_bytes < w.total) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    const NarrowWs nw = carve_narrow(mats, M, N, ws);
+    if (ws_bytes < (narrow ? nw.total : w.total)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     int num_sms, *status;
     if ((st = current_device(&num_sms, &status)) != MOE_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const double xscale = std::exp2(std::floor(0.5 * std::log2(static_cast<double>(std::max(M, N))) + 0.5));
     const size_t size = g_type == MOE_TYPE_FP32 ? 4 : 2;
     const int side = std::min(M, N);
+    if (narrow) {
+        NarrowArgs g;
+        g.G = G;
+        g.M = M;
+        g.N = N;
+        g.tiles = narrow_tiles(M, N);
+        g.interleaved = interleaved;
+        g.steps = steps;
+        g.a = a;
+        g.b = b;
+        g.c = c;
+        g.eps = eps;
+        g.xscale = xscale;
+        g.out_scale = static_cast<float>(scale / xscale);
+        g.gram_scale = static_cast<float>(kPScale / (xscale * xscale));
+        g.O = static_cast<uint16_t*>(O);
+        g.part = nw.part;
+        g.done = nw.done;
+        g.status = status;
+        const cudaError_t err = g_type == MOE_TYPE_FP32 ? launch_narrow<true>(g, nw, mats, num_sms, s)
+                                                        : launch_narrow<false>(g, nw, mats, num_sms, s);
+        return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
     for (int m0 = 0; m0 < mats; m0 += wave) {
         OrthoArgs g;
         g.M = M;

@@ -58,6 +58,25 @@ def test_one_step_matches_the_model_with_the_same_roundings(M, N, kind):
     assert ref.rel_norm(O[0].cpu(), ref.orthogonalise_model(G[0].cpu(), 1).to(torch.bfloat16)) <= 2.0 ** -9
 
 
+@pytest.mark.parametrize("M,N", [(1, 16384), (128, 128), (129, 128), (128, 129), (127, 640), (2000, 77), (90, 5000), (16384, 100)])
+def test_a_short_side(M, N):
+    # up to 128 one launch does everything; beside the limit the other kernel
+    G = torch.stack([ortho_matrix(M, N, "decay", i) for i in range(2)]).to(torch.bfloat16).cuda()
+    O = done(run(G, 2, M, N))
+    for i in range(2):
+        assert ref.rel_norm(O[i], ref.orthogonalise(G[i])) <= 2.0 ** -8 + 2.0 ** -7
+
+
+@pytest.mark.parametrize("batch,M,N,inter", [(400, 60, 70, False), (40, 128, 500, False), (200, 128, 40, True), (75, 384, 100, True),
+                                             (20, 100, 3000, False)])
+def test_many_narrow_matrices(batch, M, N, inter):
+    G = torch.randn(batch, 2 * M if inter else M, N, generator=torch.Generator("cuda").manual_seed(1), device="cuda")
+    O = done(run(G, batch, M, N, inter))
+    for i in (0, 1, batch // 2, batch - 2, batch - 1):
+        for o, x in zip(ref.split(O[i]) if inter else O[i:i + 1], ref.split(G[i]) if inter else G[i:i + 1]):
+            assert ref.rel_norm(o, ref.orthogonalise(x)) <= 2.0 ** -8 + 2.0 ** -7
+
+
 @pytest.mark.parametrize("M,N", [(128, 64), (256, 512), (384, 130), (640, 600)])
 def test_interleaved_pairs(M, N):
     pairs = torch.stack([torch.stack([ortho_matrix(M, N, "decay", 2 * i + j) for j in range(2)]) for i in range(3)])
