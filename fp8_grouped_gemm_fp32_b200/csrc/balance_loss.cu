@@ -11,13 +11,15 @@
 //
 // Both passes read each logit once, and that read bounds them when T E is large; at a step's usual size the
 // 8 MB of logits sit in L2 and launches are the time, so the forward is two launches and the backward one, each
-// set up while the one before it runs. A group of 8 or 32 lanes takes a token: the row stays in registers
-// between its maximum, its sum and its use. 32 warps an SM with one row or two each keep enough reads in
-// flight; a row costs about five instructions a value (maximum, exp2 of one fused multiply-add, sum,
-// accumulation), below the memory's pace. The forward cuts the tokens into at most 296 chunks
-// (two blocks an SM); chunk c of sequence s leaves one row of partial sums at index c + s, which is unique
-// because the cuts between chunks and sequences, taken in order, each move c or s up by one. No float is
-// added atomically, so results repeat bit for bit.
+// set up while the one before it runs. A group of 4 to 32 lanes takes a token, 16 experts a lane: the row stays
+// in registers between its maximum, its sum and its use, and the shuffles of a row are shared by the tokens of a
+// warp (131072 x 256: 40.6 us with 32 lanes a token, 33.6 with 16). 32 warps an SM keep enough reads in flight; a
+// value costs about five instructions (maximum, exp2 of one fused multiply-add, sum, accumulation), below the
+// memory's pace. The forward cuts the tokens into at most 296 chunks (two blocks an SM); chunk c of sequence s
+// leaves one row of partial sums at index c + s, which is unique because the cuts between chunks and sequences,
+// taken in order, each move c or s up by one. No float is added atomically, so results repeat bit for bit.
+// Measured on a B200, replayed: 128 x 256 forward and backward 10.6 us, 8192 x 256 13.3 us (launches); 65536 x 512
+// forward 33 us (134 MB: 4.1 TB/s, about 10 us of it the two launches' fixed cost), backward 47 us (268 MB: 5.7 TB/s).
 #include <math.h>
 
 #include <algorithm>
@@ -32,6 +34,7 @@ moe_status_t current_device(int* num_sms, int** status);
 namespace {
 
 constexpr int kFwdThreads = 512, kBwdThreads = 256;
+constexpr int kMostTokens = 1 << 30;     // a chunk past the last token still fits an int
 constexpr int kMaxChunks = 296;          // two forward blocks on each of 148 SMs
 constexpr int kBwdTokens = 16;           // tokens a backward block takes at least
 constexpr float kLog2e = 1.4426950408889634f;
@@ -145,19 +148,17 @@ __device__ __forceinline__ float group_sum(float v) {
 __device__ __forceinline__ float exp_from(float v, float c) { return exp2f(fmaf(v, kLog2e, -c)); }
 
 // ---------------------------------------------------------------- forward, pass 1: partial sums of every cut
-// U tokens of each group are in flight together.
-template <int G, int V, bool VEC, int U>
+template <int G, int V, bool VEC>
 __global__ void __launch_bounds__(kFwdThreads, 2)
 balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
                        const uint8_t* __restrict__ mask, const int32_t* __restrict__ offsets, int T, int E, int k,
                        int S, int C, BalWs w, float* __restrict__ lse) {
-    constexpr int kGroups = 32 / G, kRows = kFwdThreads / 32 * kGroups;     // tokens the block takes at a time
-    extern __shared__ float sm_red[];                               // [kRows][E]
+    constexpr int kW = kFwdThreads / 32, kRows = kW * (32 / G);     // warps; tokens the block takes at a time
+    extern __shared__ float sm_red[];                               // [kW][E]
     __shared__ int sm_hist[kMaxE];
-    __shared__ float sm_z[kRows];
-    __shared__ int sm_n[kRows];
+    __shared__ float sm_z[kW];
+    __shared__ int sm_n[kW];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % G;
-    const int row = warp * kGroups + lane / G;
     dependents_may_launch();
     wait_for_producers();
     if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0;
@@ -173,69 +174,78 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
         float z = 0.0f;
         int n = 0;
-        for (int t0 = a; t0 < b; t0 += kRows * U) {
-            float v[U][V];
-            bool on[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int t = t0 + u * kRows + row;
-                on[u] = t < b && (!mask || mask[t]);
-                load_row<G, V, VEC>(logits + static_cast<int64_t>(on[u] ? t : a) * E, E, j, -INFINITY, v[u]);
-                if (on[u])
-                    for (int i = j; i < k; i += G) {
-                        const int e = idx[static_cast<int64_t>(t) * k + i];
-                        if (e >= 0 && e < E) atomicAdd(&sm_hist[e], 1);
-                    }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                float m = v[u][0];
-#pragma unroll
-                for (int i = 1; i < V; ++i) m = fmaxf(m, v[u][i]);   // a NaN comes back through the sum
-                m = group_max<G>(m);
-                const float mc = m * kLog2e;
-                float sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    // a lane's places behind the last expert hold -inf: 0, or NaN in a row that is NaN anyway
-                    v[u][i] = exp_from(v[u][i], mc);
-                    sum += v[u][i];
-                }
-                sum = group_sum<G>(sum);
-                const int t = t0 + u * kRows + row;
-                if (on[u]) {
-                    const float r = 1.0f / sum, l = m + logf(sum);
-#pragma unroll
-                    for (int i = 0; i < V; ++i) acc[i] = fmaf(v[u][i], r, acc[i]);
-                    z = fmaf(l, l, z);
-                    ++n;
-                    if (j == 0) lse[t] = l;
-                } else if (t < b && j == 0) {
-                    lse[t] = 0.0f;
+        for (int t0 = a; t0 < b; t0 += kRows) {
+            // the row, the token's mask and its first slots in one trip to memory
+            const int t = t0 + warp * (32 / G) + lane / G, tt = t < b ? t : a;
+            float v[V];
+            load_row<G, V, VEC>(logits + static_cast<int64_t>(tt) * E, E, j, -INFINITY, v);
+            const int slot = j < k ? idx[static_cast<int64_t>(tt) * k + j] : -1;
+            const bool on = (!mask || mask[tt]) && t < b;
+            if (on) {
+                if (slot >= 0 && slot < E) atomicAdd(&sm_hist[slot], 1);
+                for (int i = j + G; i < k; i += G) {
+                    const int e = idx[static_cast<int64_t>(t) * k + i];
+                    if (e >= 0 && e < E) atomicAdd(&sm_hist[e], 1);
                 }
             }
-        }
+            float m = v[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = expert_of<G, VEC>(i, j);
-            if (e < E) sm_red[row * E + e] = acc[i];
+            for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);   // a NaN comes back through the sum
+            m = group_max<G>(m);
+            const float mc = m * kLog2e;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                // a lane's places behind the last expert hold -inf: 0, or NaN in a row that is NaN anyway
+                v[i] = exp_from(v[i], mc);
+                sum += v[i];
+            }
+            sum = group_sum<G>(sum);
+            if (on) {
+                const float r = 1.0f / sum, l = m + logf(sum);
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], r, acc[i]);
+                z = fmaf(l, l, z);
+                ++n;
+                if (j == 0) lse[t] = l;
+            } else if (t < b && j == 0) {
+                lse[t] = 0.0f;
+            }
         }
-        if (j == 0) { sm_z[row] = z; sm_n[row] = n; }
+        // the warp's token groups, then the warps
+#pragma unroll
+        for (int o = G; o < 32; o <<= 1) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+            z += __shfl_xor_sync(0xffffffffu, z, o);
+            n += __shfl_xor_sync(0xffffffffu, n, o);
+        }
+        if (lane < G) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = expert_of<G, VEC>(i, j);
+                if (e < E) sm_red[warp * E + e] = acc[i];
+            }
+        }
+        if (lane == 0) { sm_z[warp] = z; sm_n[warp] = n; }
         __syncthreads();
         const int64_t cut = static_cast<int64_t>(blockIdx.x) + s;
         for (int e = threadIdx.x; e < E; e += kFwdThreads) {
             float x = 0.0f;
-#pragma unroll 8
-            for (int r = 0; r < kRows; ++r) x += sm_red[r * E + e];
+#pragma unroll
+            for (int r = 0; r < kW; ++r) x += sm_red[r * E + e];
             w.psum[cut * E + e] = x;
             w.hist[cut * E + e] = sm_hist[e];
         }
-        if (threadIdx.x == 0) {
-            float x = 0.0f;
-            int m = 0;
-            for (int r = 0; r < kRows; ++r) { x += sm_z[r]; m += sm_n[r]; }
-            w.zsum[cut] = x;
-            w.nval[cut] = m;
+        if (warp == 0) {
+            float x = lane < kW ? sm_z[lane] : 0.0f;
+            const int m = __reduce_add_sync(0xffffffffu, lane < kW ? sm_n[lane] : 0);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+            if (lane == 0) {
+                w.zsum[cut] = x;
+                w.nval[cut] = m;
+            }
         }
         __syncthreads();
     }
@@ -357,16 +367,15 @@ balance_reduce_kernel(const int32_t* __restrict__ offsets, int T, int E, int k, 
 }
 
 // ---------------------------------------------------------------- backward
-template <int G, int V, bool VEC, int U>
+template <int G, int V, bool VEC>
 __global__ void __launch_bounds__(kBwdThreads, 4)
 balance_backward_kernel(const float* __restrict__ logits, const float* __restrict__ lse,
                         const int32_t* __restrict__ counts, const int32_t* __restrict__ valid,
                         const uint8_t* __restrict__ mask, const int32_t* __restrict__ offsets, int T, int E, int k,
                         int S, int C, float alpha, float beta, const float* __restrict__ dloss,
                         float* __restrict__ dlogits) {
-    constexpr int kGroups = 32 / G, kRows = kBwdThreads / 32 * kGroups;
+    constexpr int kRows = kBwdThreads / 32 * (32 / G);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % G;
-    const int row = warp * kGroups + lane / G;
     const int c0 = blockIdx.x * C, c1 = min(c0 + C, T);
     dependents_may_launch();
     wait_for_producers();
@@ -384,44 +393,34 @@ balance_backward_kernel(const float* __restrict__ logits, const float* __restric
             const int e = expert_of<G, VEC>(i, j);
             c[i] = e < E ? scale * static_cast<float>(counts[static_cast<int64_t>(s) * E + e]) : 0.0f;
         }
-        for (int t0 = a; t0 < b; t0 += kRows * U) {
-            float v[U][V], l[U];
-            bool on[U];
+        for (int t0 = a; t0 < b; t0 += kRows) {
+            const int t = t0 + warp * (32 / G) + lane / G;
+            const int64_t tt = t < b ? t : a;
+            const bool on = (!mask || mask[tt]) && t < b;
+            const float l = lse[tt], lc = l * kLog2e;
+            float v[V];
+            load_row<G, V, VEC>(logits + tt * E, E, j, -INFINITY, v);
+            float dot = 0.0f;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int t = t0 + u * kRows + row;
-                on[u] = t < b && (!mask || mask[t]);
-                const int64_t tt = on[u] ? t : a;
-                l[u] = lse[tt];
-                load_row<G, V, VEC>(logits + tt * E, E, j, -INFINITY, v[u]);
+            for (int i = 0; i < V; ++i) {
+                v[i] = exp_from(v[i], lc);
+                dot = fmaf(v[i], c[i], dot);
             }
+            dot = group_sum<G>(dot);
+            if (t < b) {
+                const float shift = fmaf(zc, l, -dot);
+                float* out = dlogits + static_cast<int64_t>(t) * E;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const float lc = l[u] * kLog2e;
-                float dot = 0.0f;
+                for (int i = 0; i < V; ++i) v[i] = on ? v[i] * (c[i] + shift) : 0.0f;
+                if constexpr (VEC) {
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    v[u][i] = exp_from(v[u][i], lc);
-                    dot = fmaf(v[u][i], c[i], dot);
-                }
-                dot = group_sum<G>(dot);
-                const int t = t0 + u * kRows + row;
-                if (t < b) {
-                    const float shift = fmaf(zc, l[u], -dot);
-                    float* out = dlogits + static_cast<int64_t>(t) * E;
+                    for (int q = 0; q < V / 4; ++q)
+                        if (4 * (j + G * q) < E)
+                            *reinterpret_cast<float4*>(out + 4 * (j + G * q)) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                } else {
 #pragma unroll
-                    for (int i = 0; i < V; ++i) v[u][i] = on[u] ? v[u][i] * (c[i] + shift) : 0.0f;
-                    if constexpr (VEC) {
-#pragma unroll
-                        for (int q = 0; q < V / 4; ++q)
-                            if (4 * (j + G * q) < E)
-                                *reinterpret_cast<float4*>(out + 4 * (j + G * q)) =
-                                    make_float4(v[u][4 * q], v[u][4 * q + 1], v[u][4 * q + 2], v[u][4 * q + 3]);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < V; ++i)
-                            if (j + G * i < E) out[j + G * i] = v[u][i];
-                    }
+                    for (int i = 0; i < V; ++i)
+                        if (j + G * i < E) out[j + G * i] = v[i];
                 }
             }
         }
@@ -430,15 +429,16 @@ balance_backward_kernel(const float* __restrict__ logits, const float* __restric
 
 // ---------------------------------------------------------------- launches
 // Calls f(tag) with the group size, values a lane and vector width for E experts.
-template <int G_, int V_, bool VEC_, int U_>
-struct RowForm { static constexpr int G = G_, V = V_, U = U_; static constexpr bool VEC = VEC_; };
+template <int G_, bool VEC_>
+struct RowForm { static constexpr int G = G_, V = 16; static constexpr bool VEC = VEC_; };
 
 template <typename F>
 cudaError_t with_row_form(int E, F f) {
     const bool vec = E % 4 == 0;
-    if (E <= 64) return vec ? f(RowForm<8, 8, true, 2>()) : f(RowForm<8, 8, false, 2>());
-    if (E <= 256) return vec ? f(RowForm<32, 8, true, 2>()) : f(RowForm<32, 8, false, 2>());
-    return vec ? f(RowForm<32, 16, true, 1>()) : f(RowForm<32, 16, false, 1>());
+    if (E <= 64) return vec ? f(RowForm<4, true>()) : f(RowForm<4, false>());
+    if (E <= 128) return vec ? f(RowForm<8, true>()) : f(RowForm<8, false>());
+    if (E <= 256) return vec ? f(RowForm<16, true>()) : f(RowForm<16, false>());
+    return vec ? f(RowForm<32, true>()) : f(RowForm<32, false>());
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -448,7 +448,7 @@ moe_status_t check_balance(int T, int E, int k, int S, const void* offsets, floa
     if (T < 0 || E <= 0 || k <= 0 || S <= 0 || !isfinite(alpha) || !isfinite(beta)) return MOE_ERR_INVALID_ARG;
     if (E > MOE_MAX_EXPERTS || k > MOE_MAX_TOPK || S > MOE_MAX_SEQUENCES) return MOE_ERR_UNSUPPORTED_SHAPE;
     if (k > E || (!offsets && S != 1)) return MOE_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(T) * k >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (T > kMostTokens || static_cast<int64_t>(T) * k >= (1ll << 31)) return MOE_ERR_UNSUPPORTED_SHAPE;
     return MOE_OK;
 }
 
@@ -460,7 +460,7 @@ using namespace moe;
 extern "C" {
 
 size_t moe_balance_workspace_size(int T, int E, int S) {
-    if (T < 0 || E <= 0 || E > MOE_MAX_EXPERTS || S <= 0 || S > MOE_MAX_SEQUENCES) return 0;
+    if (T < 0 || T > kMostTokens || E <= 0 || E > MOE_MAX_EXPERTS || S <= 0 || S > MOE_MAX_SEQUENCES) return 0;
     return carve_balance(T, E, S, nullptr).total;
 }
 
@@ -484,8 +484,8 @@ moe_status_t moe_balance_loss(int T, int E, int k, const float* logits, const in
     if (T > 0) {
         err = with_row_form(E, [&](auto f) {
             using F = decltype(f);
-            return launch_dependent(balance_partial_kernel<F::G, F::V, F::VEC, F::U>, dim3(chunks_of(T)), dim3(kFwdThreads),
-                                    sizeof(float) * (kFwdThreads / 32) * (32 / F::G) * E, s, logits, topk_idx, token_mask,
+            return launch_dependent(balance_partial_kernel<F::G, F::V, F::VEC>, dim3(chunks_of(T)), dim3(kFwdThreads),
+                                    sizeof(float) * (kFwdThreads / 32) * E, s, logits, topk_idx, token_mask,
                                     seq_offsets, T, E, k, S, C, w, lse);
         });
     } else {
@@ -515,9 +515,9 @@ moe_status_t moe_balance_loss_backward(int T, int E, int k, const float* logits,
     const cudaError_t err = with_row_form(E, [&](auto f) {
         using F = decltype(f);
         // a block's tokens: whole turns of its rows, several only where enough blocks are left to fill the GPU
-        const int turn = kBwdThreads / 32 * (32 / F::G) * F::U;
+        const int turn = kBwdThreads / 32 * (32 / F::G);
         const int C = std::max(std::max(kBwdTokens, turn), (T / (4 * num_sms) + turn - 1) / turn * turn);
-        return launch_dependent(balance_backward_kernel<F::G, F::V, F::VEC, F::U>, dim3((T + C - 1) / C), dim3(kBwdThreads), 0,
+        return launch_dependent(balance_backward_kernel<F::G, F::V, F::VEC>, dim3((T + C - 1) / C), dim3(kBwdThreads), 0,
                                 static_cast<cudaStream_t>(stream), logits, lse, counts, seq_valid, token_mask, seq_offsets, T,
                                 E, k, S, C, alpha, beta, dloss, dlogits);
     });

@@ -372,7 +372,8 @@ size_t moe_train_logits_offset(const moe_config_t* cfg);
  * are forced into [0, T] and reported (MOE_ERR_CAPACITY in the device status);
  * the results are then unspecified.
  * E up to MOE_MAX_EXPERTS, k up to MOE_MAX_TOPK, S up to MOE_MAX_SEQUENCES,
- * T k below 2^31 (MOE_ERR_UNSUPPORTED_SHAPE above). alpha and beta finite.
+ * T at most 2^30 and T k below 2^31 (MOE_ERR_UNSUPPORTED_SHAPE above). alpha and
+ * beta finite. The size is 0 on bad arguments.
  */
 size_t moe_balance_workspace_size(int T, int E, int S);
 moe_status_t moe_balance_loss(int T, int E, int k, const float* logits, const int32_t* topk_idx,
@@ -401,14 +402,15 @@ moe_status_t moe_balance_loss_backward(int T, int E, int k, const float* logits,
  *   db  [E]    fp32 = db0  + column sums of dlogits
  *   x [T, H] bf16, Wg [E, H] fp32, dlogits [T, E] fp32
  *   dx0, dWg0, db0  nullable (0): gradients to add to, moe_backward's; each may
- *                   be its output
+ *                   be its output (otherwise outputs overlap nothing)
  *   ws  scratch of moe_router_backward_workspace_size(T, H, E) bytes, 256-byte
  *       aligned
  * The products run on the tensor cores: dWg with dlogits in three bf16 parts
  * (its 24 bits) against x, sums promoted to fp32 registers every 128 tokens;
- * dx with W_g and dlogits in fp16 (11 bits, an eighth of dx's own rounding
- * step), each expert and then each token scaled by a power of two. Results
- * repeat bit for bit. A dlogits row of zeros leaves its dx row at dx0. Values
+ * dx up to 128 experts with W_g and dlogits in bf16 pairs (16 bits), above in
+ * fp16 (11 bits, an eighth of dx's own rounding step), each expert and then each
+ * token scaled by a power of two. Up to 512 tokens and 2^25 products T H E both
+ * run in fp32 on the CUDA cores. Results repeat bit for bit. A dlogits row of zeros leaves its dx row at dx0. Values
  * that are not finite spread only as the formulas spread them, except that an
  * expert whose W_g row holds one makes every dx row NaN or infinite. T = 0 gives the
  * bases, or zeros.
@@ -440,13 +442,15 @@ moe_status_t moe_router_backward(int T, int H, int E, const void* x, const float
  *               waves that use it in turn
  * Products are fp16 with fp32 sums; X is carried in 22 bits, so that the
  * result differs from exact arithmetic by about bf16's own rounding also where
- * G is of low rank. A matrix of zeros (with eps > 0) gives zeros; a matrix
+ * G is of low rank. Large matrices (both sides from 1024, one at least 1.5 times
+ * the other) take their first two steps at once, in products of the smaller
+ * Gram matrix: the same iterate, other roundings. A matrix of zeros (with eps > 0) gives zeros; a matrix
  * with an infinity or a NaN gives NaN, the others of the batch are unaffected.
  * The coefficients must keep the singular values below 8 and |b x^2 + c x^4|
  * below 256 from any start in [0, 1] (MOE_ERR_INVALID_ARG otherwise: X would
  * leave fp16). M, N and batch from 1 (batch 0: nothing is done) to 16384
- * (MOE_ERR_UNSUPPORTED_SHAPE above). Results repeat bit for bit. The kernel is
- * a cooperative launch of one block per SM.
+ * (MOE_ERR_UNSUPPORTED_SHAPE above). Results repeat bit for bit. The kernels are
+ * cooperative launches of at most one block per SM.
  */
 size_t moe_orthogonalise_workspace_size(int batch, int M, int N, int interleaved);
 moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const void* G, int g_type, int steps, float a,

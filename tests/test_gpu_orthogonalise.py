@@ -174,18 +174,41 @@ def test_repeats_on_another_stream_and_two_at_once():
     assert all(torch.equal(o, want) for o in outs)
 
 
-def test_captured_and_replayed_on_new_inputs():
-    G = torch.stack([ortho_matrix(200, 140, "decay", i) for i in range(2)]).cuda()
-    ws = torch.empty(api.moe_orthogonalise_workspace_size(2, 200, 140), dtype=torch.uint8, device="cuda")
-    O = run(G, 2, 200, 140, ws=ws)
+@pytest.mark.parametrize("M,N", [(200, 140), (64, 64), (100, 700), (1030, 1700)])
+def test_captured_and_replayed_on_new_inputs(M, N):
+    G = torch.stack([ortho_matrix(M, N, "decay", i) for i in range(2)]).cuda()
+    ws = torch.empty(api.moe_orthogonalise_workspace_size(2, M, N), dtype=torch.uint8, device="cuda")
+    O = run(G, 2, M, N, ws=ws)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g, stream=torch.cuda.Stream()):
-        run(G, 2, 200, 140, ws=ws, O=O)
+        run(G, 2, M, N, ws=ws, O=O)
     for k in range(2):
-        G.copy_(torch.stack([ortho_matrix(200, 140, "noise", 10 * k + i) for i in range(2)]))
+        G.copy_(torch.stack([ortho_matrix(M, N, "noise", 10 * k + i) for i in range(2)]))
         torch.cuda.synchronize()
         g.replay()
         done(O)
         for i in range(2):
-            close(O[i], G[i])
+            assert ref.rel_norm(O[i], ref.orthogonalise(G[i])) <= 2.0 ** -8 + 2.0 ** -7
+
+
+def test_two_graphs_with_their_own_workspaces_at_once():
+    shapes = [(100, 700), (300, 520)]
+    graphs, outs, wants = [], [], []
+    for M, N in shapes:
+        G = torch.stack([ortho_matrix(M, N, "decay", i) for i in range(3)]).cuda()
+        ws = torch.empty(api.moe_orthogonalise_workspace_size(3, M, N), dtype=torch.uint8, device="cuda")
+        wants.append(done(run(G, 3, M, N, ws=ws)).clone())
+        O = torch.zeros_like(wants[-1])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=torch.cuda.Stream()):
+            run(G, 3, M, N, ws=ws, O=O)
+        graphs.append((g, G, ws))
+        outs.append(O)
+    streams = [torch.cuda.Stream() for _ in shapes]
+    for _ in range(3):
+        for (g, _, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    done(outs[0])
+    assert all(torch.equal(o, w) for o, w in zip(outs, wants))

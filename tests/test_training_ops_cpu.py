@@ -103,7 +103,7 @@ def ortho_matrix(M, N, kind, seed):
 def test_workspace_sizes(L):
     assert api.moe_balance_workspace_size(8192, 256, 1) > 0
     assert api.moe_balance_workspace_size(0, 8, 1) > 0
-    for bad in ((-1, 8, 1), (8, 0, 1), (8, 513, 1), (8, 8, 0), (8, 8, 65536)):
+    for bad in ((-1, 8, 1), ((1 << 30) + 1, 8, 1), (8, 0, 1), (8, 513, 1), (8, 8, 0), (8, 8, 65536)):
         assert api.moe_balance_workspace_size(*bad) == 0
     assert api.moe_router_backward_workspace_size(8192, 7168, 256) > 0
     for bad in ((-1, 128, 8), (8, 100, 8), (8, 128, 513), (8, 16512, 8), (1 << 24, 128, 8), (8, 0, 8), (8, 128, 0)):
@@ -134,7 +134,7 @@ BAL = dict(T=64, E=8, k=2, logits=OKP, idx=OKP, mask=0, off=0, S=1, alpha=0.01, 
 @pytest.mark.parametrize("change,code", [
     (dict(T=-1), INVALID), (dict(E=0), INVALID), (dict(k=0), INVALID), (dict(S=0), INVALID), (dict(k=9), INVALID),
     (dict(E=513, k=2), SHAPE), (dict(E=64, k=33), SHAPE), (dict(S=65536, off=OKP), SHAPE), (dict(S=2), INVALID),
-    (dict(T=1 << 30), SHAPE), (dict(alpha=float("nan")), INVALID), (dict(beta=float("inf")), INVALID),
+    (dict(T=1 << 30), SHAPE), (dict(T=(1 << 30) + 1, E=8, k=1), SHAPE), (dict(alpha=float("nan")), INVALID), (dict(beta=float("inf")), INVALID),
     (dict(logits=0), INVALID), (dict(logits=ODD), INVALID), (dict(idx=0), INVALID), (dict(mask=ODD), INVALID),
     (dict(off=ODD), INVALID), (dict(loss=0), INVALID), (dict(counts=ODD), INVALID), (dict(mp=0), INVALID),
     (dict(lse=0), INVALID), (dict(valid=0), INVALID), (dict(ws=0), INVALID), (dict(nbytes=16), SMALL)])
