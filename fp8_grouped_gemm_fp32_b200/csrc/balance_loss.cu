@@ -10,15 +10,15 @@
 //   dl_t[e] = p_t[e] (c[s, e] - sum_j p_t[j] c[s, j]) + 2 g1 beta / N lse_t p_t[e].
 //
 // Both passes read each logit once, and that read bounds them when T E is large; at a step's usual size the
-// 8 MB of logits sit in L2 and launches are the time, so the forward is two launches and the backward one, each
-// set up while the one before it runs. A group of 4 to 32 lanes takes a token, 16 experts a lane: the row stays
+// 8 MB of logits sit in L2 and launches are the time, so the forward is two launches (one for few tokens) and the
+// backward one, each set up while the one before it runs. A group of 4 to 32 lanes takes a token, 16 experts a lane: the row stays
 // in registers between its maximum, its sum and its use, and the shuffles of a row are shared by the tokens of a
 // warp (131072 x 256: 40.6 us with 32 lanes a token, 33.6 with 16). 32 warps an SM keep enough reads in flight; a
 // value costs about five instructions (maximum, exp2 of one fused multiply-add, sum, accumulation), below the
 // memory's pace. The forward cuts the tokens into at most 296 chunks (two blocks an SM); chunk c of sequence s
 // leaves one row of partial sums at index c + s, which is unique because the cuts between chunks and sequences,
 // taken in order, each move c or s up by one. No float is added atomically, so results repeat bit for bit.
-// Measured on a B200, replayed: 128 x 256 forward and backward 10.6 us, 8192 x 256 13.3 us (launches); 65536 x 512
+// Measured on a B200, replayed: 128 x 256 forward and backward 9.8 us, 8192 x 256 13.3 us (launches); 65536 x 512
 // forward 33 us (134 MB: 4.1 TB/s, about 10 us of it the two launches' fixed cost), backward 47 us (268 MB: 5.7 TB/s).
 #include <math.h>
 
@@ -147,21 +147,24 @@ __device__ __forceinline__ float group_sum(float v) {
 // exp(v - m) as 2^(v log2 e - m log2 e); c = m log2 e. Rounding c scales a whole row alike, which its sum undoes.
 __device__ __forceinline__ float exp_from(float v, float c) { return exp2f(fmaf(v, kLog2e, -c)); }
 
+__device__ __forceinline__ double warp_sum(double v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
 // ---------------------------------------------------------------- forward, pass 1: partial sums of every cut
 template <int G, int V, bool VEC>
-__global__ void __launch_bounds__(kFwdThreads, 2)
-balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
-                       const uint8_t* __restrict__ mask, const int32_t* __restrict__ offsets, int T, int E, int k,
-                       int S, int C, BalWs w, float* __restrict__ lse) {
+__device__ __forceinline__ void
+partial_sums(const float* __restrict__ logits, const int32_t* __restrict__ idx, const uint8_t* __restrict__ mask,
+             const int32_t* __restrict__ offsets, int T, int E, int k, int S, int C, const BalWs& w,
+             float* __restrict__ lse) {
     constexpr int kW = kFwdThreads / 32, kRows = kW * (32 / G);     // warps; tokens the block takes at a time
     extern __shared__ float sm_red[];                               // [kW][E]
     __shared__ int sm_hist[kMaxE];
     __shared__ float sm_z[kW];
     __shared__ int sm_n[kW];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % G;
-    dependents_may_launch();
-    wait_for_producers();
-    if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0;
     const int c0 = blockIdx.x * C, c1 = min(c0 + C, T);
     for (int s = seq_behind(offsets, S, T, c0); s < S; ++s) {
         const int a = max(seq_start(offsets, s, T), c0), b = min(seq_start(offsets, s + 1, T), c1);
@@ -251,10 +254,104 @@ balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restri
     }
 }
 
-__device__ __forceinline__ double warp_sum(double v) {
+template <int G, int V, bool VEC>
+__global__ void __launch_bounds__(kFwdThreads, 2)
+balance_partial_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
+                       const uint8_t* __restrict__ mask, const int32_t* __restrict__ offsets, int T, int E, int k,
+                       int S, int C, BalWs w, float* __restrict__ lse) {
+    dependents_may_launch();
+    wait_for_producers();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *w.ticket = 0;
+    partial_sums<G, V, VEC>(logits, idx, mask, offsets, T, E, k, S, C, w, lse);
+}
+
+// The blocks' shares of the losses, added in a fixed order by one block of W warps.
+template <int W>
+__device__ __forceinline__ void finish_losses(const BalWs& w, int S, int nx, int E, int k, float alpha, float beta,
+                                              float* __restrict__ loss, int32_t* valid) {
+    __shared__ double sm_0[W], sm_1[W];
+    __shared__ int sm_f[W], sm_t[W];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    double l0 = 0.0, l1 = 0.0;
+    int full = 0, total = 0;
+    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(S) * nx; i += 32 * W) l0 += __ldcg(w.part + i);
+    for (int i = threadIdx.x; i < S; i += 32 * W) {
+        const int v = __ldcg(valid + i);
+        l1 += __ldcg(w.zpart + i);
+        full += v > 0;
+        total += v;
+    }
+    l0 = warp_sum(l0);
+    l1 = warp_sum(l1);
+    full = __reduce_add_sync(0xffffffffu, full);
+    total = __reduce_add_sync(0xffffffffu, total);
+    if (lane == 0) { sm_0[warp] = l0; sm_1[warp] = l1; sm_f[warp] = full; sm_t[warp] = total; }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        l0 = l1 = 0.0;
+        full = total = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
+        for (int i = 0; i < W; ++i) { l0 += sm_0[i]; l1 += sm_1[i]; full += sm_f[i]; total += sm_t[i]; }
+        loss[0] = static_cast<float>(alpha * l0 * E / (static_cast<double>(k) * max(full, 1)));
+        loss[1] = static_cast<float>(beta * l1 / max(total, 1));
+        valid[S] = full;
+        valid[S + 1] = total;
+    }
+}
+
+// Offsets that are not non-decreasing within [0, T] are reported.
+__device__ __forceinline__ void check_offsets(const int32_t* offsets, int s, int a, int b, int* status) {
+    if (offsets && (offsets[s] != a || offsets[s + 1] != b || a > b)) set_status(status, kStatusCapacity);
+}
+
+// Few tokens: the whole forward as one cluster of up to 8 blocks, a chunk each; then a warp takes 32 columns of a
+// sequence over its few cuts, and the first block the losses. One launch less on the host (2 us), and 7.2 us instead of
+// 7.9 on the GPU at 128 x 256; at 512 x 512 eight SMs are too few (10.4 us against 8.6).
+constexpr int kSmallTokens = 256, kSmallBlocks = 8;
+template <int G, int V, bool VEC>
+__global__ void __launch_bounds__(kFwdThreads)
+balance_small_kernel(const float* __restrict__ logits, const int32_t* __restrict__ idx,
+                     const uint8_t* __restrict__ mask, const int32_t* __restrict__ offsets, int T, int E, int k, int S,
+                     int C, BalWs w, float* __restrict__ lse, float alpha, float beta, float* __restrict__ loss,
+                     int32_t* __restrict__ counts, float* __restrict__ mean_prob, int32_t* valid, int* status) {
+    constexpr int kW = kFwdThreads / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nx = (E + 31) / 32;
+    dependents_may_launch();
+    wait_for_producers();
+    partial_sums<G, V, VEC>(logits, idx, mask, offsets, T, E, k, S, C, w, lse);
+    __syncwarp();
+    cluster_sync();                                     // every block's cuts are in memory
+    for (int item = blockIdx.x * kW + warp; item < S * nx; item += gridDim.x * kW) {
+        const int s = item / nx, x = item - s * nx, e = x * 32 + lane;
+        const int a = seq_start(offsets, s, T), b = seq_start(offsets, s + 1, T);
+        if (x == 0 && lane == 0) check_offsets(offsets, s, a, b, status);
+        const int lo = a / C, hi = b > a ? (b - 1) / C + 1 : lo;
+        double p = 0.0;
+        int h = 0;
+#pragma unroll
+        for (int i = 0; i < kSmallBlocks; ++i) {
+            const bool in = lo + i < hi && e < E;
+            const int64_t at = (static_cast<int64_t>(lo) + i + s) * E + e;
+            p += in ? __ldcg(w.psum + at) : 0.0f;
+            h += in ? __ldcg(w.hist + at) : 0;
+        }
+        const bool mine = lo + lane < hi;
+        const int n = __reduce_add_sync(0xffffffffu, mine ? __ldcg(w.nval + lo + lane + s) : 0);
+        const double z = warp_sum(mine ? __ldcg(w.zsum + lo + lane + s) : 0.0f);
+        const double inv = n > 0 ? 1.0 / n : 0.0;
+        if (e < E) {
+            mean_prob[static_cast<int64_t>(s) * E + e] = static_cast<float>(p * inv);
+            counts[static_cast<int64_t>(s) * E + e] = h;
+        }
+        const double share = warp_sum(e < E ? p * h * inv * inv : 0.0);
+        if (lane == 0) {
+            w.part[item] = share;
+            if (x == 0) { w.zpart[s] = z; valid[s] = n; }
+        }
+    }
+    __syncwarp();
+    cluster_sync();
+    if (blockIdx.x == 0) finish_losses<kW>(w, S, nx, E, k, alpha, beta, loss, valid);
 }
 
 // ---------------------------------------------------------------- forward, pass 2: the cuts of each sequence
@@ -268,8 +365,8 @@ balance_reduce_kernel(const int32_t* __restrict__ offsets, int T, int E, int k, 
     constexpr int kRows = kRedThreads / COLS, kW = kRedThreads / 32;
     __shared__ float sm_p[kW][COLS];
     __shared__ int sm_h[kW][COLS];
-    __shared__ double sm_z[kW], sm_z2[kW];
-    __shared__ int sm_n[kW], sm_n2[kW];
+    __shared__ double sm_z[kW];
+    __shared__ int sm_n[kW];
     __shared__ bool sm_last;
     const int col = threadIdx.x % COLS, r0 = threadIdx.x / COLS, s = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -277,8 +374,7 @@ balance_reduce_kernel(const int32_t* __restrict__ offsets, int T, int E, int k, 
     dependents_may_launch();
     wait_for_producers();
     const int a = seq_start(offsets, s, T), b = seq_start(offsets, s + 1, T);
-    if (offsets && threadIdx.x == 0 && blockIdx.x == 0 && (offsets[s] != a || offsets[s + 1] != b || a > b))
-        set_status(status, kStatusCapacity);
+    if (threadIdx.x == 0 && blockIdx.x == 0) check_offsets(offsets, s, a, b, status);
     const int lo = a / C, hi = b > a ? (b - 1) / C + 1 : lo;       // chunks that hold some of the sequence
     float p = 0.0f;
     int h = 0, n = 0;
@@ -339,31 +435,7 @@ balance_reduce_kernel(const int32_t* __restrict__ offsets, int T, int E, int k, 
     __syncthreads();
     if (!sm_last) return;
     __threadfence();
-    double l0 = 0.0, l1 = 0.0;
-    int full = 0, total = 0;
-    for (int64_t i = threadIdx.x; i < static_cast<int64_t>(S) * gridDim.x; i += kRedThreads) l0 += __ldcg(w.part + i);
-    for (int i = threadIdx.x; i < S; i += kRedThreads) {
-        const int v = __ldcg(valid + i);
-        l1 += __ldcg(w.zpart + i);
-        full += v > 0;
-        total += v;
-    }
-    l0 = warp_sum(l0);
-    l1 = warp_sum(l1);
-    full = __reduce_add_sync(0xffffffffu, full);
-    total = __reduce_add_sync(0xffffffffu, total);
-    if (lane == 0) { sm_z[warp] = l0; sm_z2[warp] = l1; sm_n[warp] = full; sm_n2[warp] = total; }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        l0 = l1 = 0.0;
-        full = total = 0;
-#pragma unroll
-        for (int i = 0; i < kW; ++i) { l0 += sm_z[i]; l1 += sm_z2[i]; full += sm_n[i]; total += sm_n2[i]; }
-        loss[0] = static_cast<float>(alpha * l0 * E / (static_cast<double>(k) * max(full, 1)));
-        loss[1] = static_cast<float>(beta * l1 / max(total, 1));
-        valid[S] = full;
-        valid[S + 1] = total;
-    }
+    finish_losses<kW>(w, S, gridDim.x, E, k, alpha, beta, loss, valid);
 }
 
 // ---------------------------------------------------------------- backward
@@ -481,6 +553,29 @@ moe_status_t moe_balance_loss(int T, int E, int k, const float* logits, const in
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int C = chunk_tokens(T);
     cudaError_t err;
+    if (T > 0 && T <= kSmallTokens) {
+        const int Cs = std::max(16, (T + 16 * kSmallBlocks - 1) / (16 * kSmallBlocks) * 16), blocks = (T + Cs - 1) / Cs;
+        err = with_row_form(E, [&](auto f) {
+            using F = decltype(f);
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[2];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            attr[1].id = cudaLaunchAttributeClusterDimension;
+            attr[1].val.clusterDim.x = blocks;
+            attr[1].val.clusterDim.y = 1;
+            attr[1].val.clusterDim.z = 1;
+            cfg.gridDim = dim3(blocks);
+            cfg.blockDim = dim3(kFwdThreads);
+            cfg.dynamicSmemBytes = sizeof(float) * (kFwdThreads / 32) * E;
+            cfg.stream = s;
+            cfg.attrs = attr;
+            cfg.numAttrs = 2;
+            return cudaLaunchKernelEx(&cfg, balance_small_kernel<F::G, F::V, F::VEC>, logits, topk_idx, token_mask, seq_offsets, T,
+                                      E, k, S, Cs, w, lse, alpha, beta, loss, counts, mean_prob, seq_valid, status);
+        });
+        return err == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
     if (T > 0) {
         err = with_row_form(E, [&](auto f) {
             using F = decltype(f);

@@ -71,15 +71,16 @@ class Case:
 
 
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 8), (2, 7, 3), (63, 64, 2), (129, 65, 4), (300, 256, 8), (257, 257, 1),
-                                   (513, 512, 32), (1000, 4, 2), (2500, 30, 3), (5000, 128, 8)])
+                                   (513, 512, 32), (1000, 4, 2), (2500, 30, 3), (5000, 128, 8), (16, 200, 9), (17, 16, 2), (128, 256, 8),
+                                   (129, 511, 31), (500, 90, 5), (512, 512, 8)])
 def test_one_sequence(T, E, k):
     Case(T, E, k).forward().backward().check()
 
 
-@pytest.mark.parametrize("E", [8, 60, 61, 256, 300, 511])
-def test_ragged_masked_sequences_with_rows_behind_the_last(E):
+@pytest.mark.parametrize("E", [8, 60, 61, 100, 256, 300, 511])
+@pytest.mark.parametrize("T", [250, 1500])
+def test_ragged_masked_sequences_with_rows_behind_the_last(E, T):
     r = np.random.default_rng(E)
-    T = 1500
     cuts = np.sort(r.integers(3, T - 40, 40))
     off = [3, 3, *cuts, cuts[-1], cuts[-1] + 1]           # empty ones, a sequence of one token, rows left and right
     mask = (r.random(T) > 0.3).astype(np.uint8)
@@ -88,8 +89,8 @@ def test_ragged_masked_sequences_with_rows_behind_the_last(E):
     c.forward().backward(torch.tensor([0.5, -2.0], device="cuda")).check((0.5, -2.0))
 
 
-def test_every_token_its_own_sequence():
-    T = 700
+@pytest.mark.parametrize("T", [250, 700])
+def test_every_token_its_own_sequence(T):
     Case(T, 16, 2, off=list(range(T + 1))).forward().backward().check()
 
 
@@ -105,8 +106,9 @@ def test_no_valid_token_and_no_token():
     c.forward().backward().check()
 
 
-def test_masked_rows_may_hold_anything_and_minus_infinity_is_a_zero_probability():
-    T, E = 200, 40
+@pytest.mark.parametrize("T", [200, 900])
+def test_masked_rows_may_hold_anything_and_minus_infinity_is_a_zero_probability(T):
+    E = 40
     r = np.random.default_rng(5)
     logits = r.normal(size=(T, E)).astype(np.float32)
     mask = np.ones(T, np.uint8)
@@ -141,8 +143,9 @@ def test_an_undefined_row_stays_in_its_sequence():
     assert np.isfinite(np.delete(dl, [40, 70], 0)).all() and np.isnan(dl[40]).all() and np.isnan(dl[70]).all()
 
 
-def test_slots_outside_the_experts_count_nowhere():
-    c = Case(100, 8, 4)
+@pytest.mark.parametrize("T", [100, 800])
+def test_slots_outside_the_experts_count_nowhere(T):
+    c = Case(T, 8, 4)
     c.idx[::3, 1] = -1
     c.idx[1::3, 2] = 8
     c.idx[2::3, 0] = 2 ** 31 - 1
@@ -151,21 +154,23 @@ def test_slots_outside_the_experts_count_nowhere():
 
 
 @pytest.mark.parametrize("off", [[0, 50, 40, 90], [-5, 50, 60, 90], [0, 50, 60, 1000], [90, 50, 20, 0]])
-def test_bad_offsets_are_reported_and_stay_in_bounds(off):
-    c = Case(90, 16, 2, off=[0, 30, 60, 90])
+@pytest.mark.parametrize("T", [90, 400])
+def test_bad_offsets_are_reported_and_stay_in_bounds(off, T):
+    c = Case(T, 16, 2, off=[0, 30, 60, T])
     c.d_off.copy_(torch.tensor(off, dtype=torch.int32))
     c.forward().backward()
     torch.cuda.synchronize()
     assert api.moe_get_device_status() == api.MOE_ERR_CAPACITY
 
 
-def test_results_repeat_bit_for_bit_and_on_another_stream():
-    c = Case(4000, 100, 6, off=[0, 100, 2500, 3999])
+@pytest.mark.parametrize("T", [200, 4000])
+def test_results_repeat_bit_for_bit_and_on_another_stream(T):
+    c = Case(T, 100, 6, off=[0, 100, T // 2 + 50, T - 1])
     first = c.forward().backward().results()
     s = torch.cuda.Stream()
     s.wait_stream(torch.cuda.current_stream())
     for st in (None, s):
-        for t in (c.loss, c.mp, c.dl[:3999]):
+        for t in (c.loss, c.mp, c.dl[:T - 1]):
             t.fill_(7)
         torch.cuda.synchronize()
         again = c.forward(st).backward(stream=st).results()
@@ -173,8 +178,9 @@ def test_results_repeat_bit_for_bit_and_on_another_stream():
             assert np.array_equal(x, y)
 
 
-def test_captured_and_replayed_on_new_inputs():
-    c = Case(3000, 64, 2, off=[0, 1000, 3000])
+@pytest.mark.parametrize("T", [240, 3000])
+def test_captured_and_replayed_on_new_inputs(T):
+    c = Case(T, 64, 2, off=[0, 100, T])
     s = torch.cuda.Stream()
     c.forward().backward()
     torch.cuda.synchronize()
