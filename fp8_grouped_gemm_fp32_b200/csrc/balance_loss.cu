@@ -52,7 +52,7 @@ int red_cols(int S) { return S <= 16 ? 8 : 32; }
 struct BalWs {
     float* psum;        // [cuts, E] sums of p
     int32_t* hist;      // [cuts, E] slots
-    float* zsum;        // [cuts] sums of lse^2
+    double* zsum;       // [cuts] sums of lse^2: a row far from zero has one outside fp32
     int32_t* nval;      // [cuts] valid tokens
     double* part;       // [S, column blocks] sum_e counts * psum over the block's columns
     double* zpart;      // [S]
@@ -72,7 +72,7 @@ BalWs carve_balance(int T, int E, int S, void* base) {
     };
     w.psum = reinterpret_cast<float*>(take(4 * cuts * E));
     w.hist = reinterpret_cast<int32_t*>(take(4 * cuts * E));
-    w.zsum = reinterpret_cast<float*>(take(4 * cuts));
+    w.zsum = reinterpret_cast<double*>(take(8 * cuts));
     w.nval = reinterpret_cast<int32_t*>(take(4 * cuts));
     w.part = reinterpret_cast<double*>(take(8 * static_cast<size_t>(S) * nx));
     w.zpart = reinterpret_cast<double*>(take(8 * static_cast<size_t>(S)));
@@ -147,6 +147,11 @@ __device__ __forceinline__ float group_sum(float v) {
 // exp(v - m) as 2^(v log2 e - m log2 e); c = m log2 e. Rounding c scales a whole row alike, which its sum undoes.
 __device__ __forceinline__ float exp_from(float v, float c) { return exp2f(fmaf(v, kLog2e, -c)); }
 
+// Rows whose maximum or lse is farther than this from zero (all of a row at the type's lowest value, say) are shifted to
+// it first: the rounding of c shows in lse, as much as lse's own, and from about 2^30 on would leave exp2's range; the
+// gradient, which has no sum to undo them, would show that of c and of lse.
+constexpr float kFar = 64.0f;
+
 __device__ __forceinline__ double warp_sum(double v) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -162,7 +167,7 @@ partial_sums(const float* __restrict__ logits, const int32_t* __restrict__ idx, 
     constexpr int kW = kFwdThreads / 32, kRows = kW * (32 / G);     // warps; tokens the block takes at a time
     extern __shared__ float sm_red[];                               // [kW][E]
     __shared__ int sm_hist[kMaxE];
-    __shared__ float sm_z[kW];
+    __shared__ double sm_z[kW];
     __shared__ int sm_n[kW];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % G;
     const int c0 = blockIdx.x * C, c1 = min(c0 + C, T);
@@ -175,7 +180,7 @@ partial_sums(const float* __restrict__ logits, const int32_t* __restrict__ idx, 
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-        float z = 0.0f;
+        double z = 0.0;
         int n = 0;
         for (int t0 = a; t0 < b; t0 += kRows) {
             // the row, the token's mask and its first slots in one trip to memory
@@ -195,7 +200,12 @@ partial_sums(const float* __restrict__ logits, const int32_t* __restrict__ idx, 
 #pragma unroll
             for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);   // a NaN comes back through the sum
             m = group_max<G>(m);
-            const float mc = m * kLog2e;
+            float mc = m * kLog2e;
+            if (fabsf(m) > kFar) {
+                mc = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) v[i] -= m;
+            }
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -208,7 +218,7 @@ partial_sums(const float* __restrict__ logits, const int32_t* __restrict__ idx, 
                 const float r = 1.0f / sum, l = m + logf(sum);
 #pragma unroll
                 for (int i = 0; i < V; ++i) acc[i] = fmaf(v[i], r, acc[i]);
-                z = fmaf(l, l, z);
+                z = fma(static_cast<double>(l), static_cast<double>(l), z);
                 ++n;
                 if (j == 0) lse[t] = l;
             } else if (t < b && j == 0) {
@@ -241,10 +251,8 @@ partial_sums(const float* __restrict__ logits, const int32_t* __restrict__ idx, 
             w.hist[cut * E + e] = sm_hist[e];
         }
         if (warp == 0) {
-            float x = lane < kW ? sm_z[lane] : 0.0f;
+            const double x = warp_sum(lane < kW ? sm_z[lane] : 0.0);
             const int m = __reduce_add_sync(0xffffffffu, lane < kW ? sm_n[lane] : 0);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
             if (lane == 0) {
                 w.zsum[cut] = x;
                 w.nval[cut] = m;
@@ -337,7 +345,7 @@ balance_small_kernel(const float* __restrict__ logits, const int32_t* __restrict
         }
         const bool mine = lo + lane < hi;
         const int n = __reduce_add_sync(0xffffffffu, mine ? __ldcg(w.nval + lo + lane + s) : 0);
-        const double z = warp_sum(mine ? __ldcg(w.zsum + lo + lane + s) : 0.0f);
+        const double z = warp_sum(mine ? __ldcg(w.zsum + lo + lane + s) : 0.0);
         const double inv = n > 0 ? 1.0 / n : 0.0;
         if (e < E) {
             mean_prob[static_cast<int64_t>(s) * E + e] = static_cast<float>(p * inv);
@@ -469,9 +477,26 @@ balance_backward_kernel(const float* __restrict__ logits, const float* __restric
             const int t = t0 + warp * (32 / G) + lane / G;
             const int64_t tt = t < b ? t : a;
             const bool on = (!mask || mask[tt]) && t < b;
-            const float l = lse[tt], lc = l * kLog2e;
+            const float l = lse[tt];
+            float lc = l * kLog2e;
             float v[V];
             load_row<G, V, VEC>(logits + tt * E, E, j, -INFINITY, v);
+            const bool far = fabsf(l) > kFar;
+            if (__any_sync(0xffffffffu, far)) {
+                float m = v[0];
+#pragma unroll
+                for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
+                m = group_max<G>(m);
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum += exp2f((v[i] - m) * kLog2e);
+                sum = group_sum<G>(sum);
+                if (far) {
+                    lc = log2f(sum);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[i] -= m;
+                }
+            }
             float dot = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {

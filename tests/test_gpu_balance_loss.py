@@ -217,3 +217,58 @@ def test_gradient_against_differences():
             num = (vals[0] - vals[1]) / (2 * step)
             assert abs(num - dl[t, e]) <= 2 * 64 * U * abs(vals[0]) / step + 4 * step ** 2, (t, e)
     c.d_logits.copy_(torch.from_numpy(c.logits))
+
+
+@pytest.mark.parametrize("T,E", [(60, 7), (100, 64), (700, 130), (600, 512)])
+def test_rows_far_from_zero(T, E):
+    # Rows shifted by up to 2^30 and rows with every logit at the type's lowest value (p = 1 / E). A row's probabilities
+    # depend on its differences alone, whose size is at most d for all that are not negligible: (2 d + 16) u relative.
+    r = np.random.default_rng(T)
+    logits = r.normal(size=(T, E)).astype(np.float32)
+    for t in range(T):
+        shift = [0.0, 70.0, -70.0, 3e3, -3e3, 2e6, -2e6, 2.0 ** 30, -2.0 ** 30][t % 9]
+        logits[t] += np.float32(shift)
+    logits[5] = logits[20] = np.finfo(np.float32).min
+    logits[21, 1:] = np.finfo(np.float32).min
+    d = 128 * 1.5                                           # 2^30 + x keeps x to multiples of 64 or 128
+    c = Case(T, E, min(3, E), logits=logits, beta=0.0).forward().backward()
+    loss, counts, mp, lse, valid, dl = c.results()
+    want = ref.balance(logits, c.idx, None, [0, T], c.alpha, 0.0, c.k)
+    assert np.array_equal(counts, want["counts"])
+    assert (np.abs(mp - want["mean_prob"]) <= (2 * d + 112) * U * want["mean_prob"]).all()
+    assert abs(loss[0] - want["loss"][0]) <= (2 * d + 112) * U * want["loss"][0] and loss[1] == 0
+    assert (np.abs(lse - want["lse"]) <= (2 * d + 16) * U + U * np.abs(want["lse"])).all()
+    g, mag = ref.balance_grad(want, [0, T], c.alpha, 0.0, c.k)
+    # rows within 64 of zero take p from lse as it was rounded: 64 more steps of u, twice
+    assert (np.abs(dl - g) <= (4 * d + 64 + 256) * U * mag).all()
+    c.beta = 1e-3                                           # the z-loss leaves fp32, its gradient does not
+    c.forward().backward()
+    loss, counts, mp, lse, valid, dl = c.results()
+    want = ref.balance(logits, c.idx, None, [0, T], c.alpha, c.beta, c.k)
+    g, mag = ref.balance_grad(want, [0, T], c.alpha, c.beta, c.k)
+    assert loss[1] == np.inf and (np.abs(dl - g) <= (4 * d + 64 + 256) * U * mag).all()
+
+
+@pytest.mark.parametrize("T", [0, 100, 900])
+def test_captured_behind_a_memset_a_copy_and_a_joined_stream(T):
+    c = Case(T, 64, 2)
+    want = c.forward().backward().results()
+    src, s, side = c.d_logits.clone(), torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        c.lse.zero_()
+        side.wait_stream(s)
+        with torch.cuda.stream(side):
+            c.dl.fill_(3)
+        c.d_logits.copy_(src)
+        s.wait_stream(side)
+        c.forward()
+        c.loss.add_(0.0)
+        c.backward()
+    for _ in range(2):
+        for t in (c.loss, c.counts, c.mp, c.d_logits):
+            t.fill_(7)
+        g.replay()
+        for x, y in zip(want, c.results()):
+            assert np.array_equal(x, y)

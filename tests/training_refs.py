@@ -18,7 +18,7 @@ def balance(logits, idx, mask, off, alpha, beta, k, counts=None):
     with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
         ex = np.exp(l - m[:, None])
         lse = m + np.log(ex.sum(1))
-        p = np.exp(l - lse[:, None])
+        p = ex / ex.sum(1, keepdims=True)      # exp(l - lse) would lose log E beside lowest values
     keep = np.ones(T, bool) if mask is None else np.asarray(mask) != 0
     cnt, mp, n = np.zeros((S, E)), np.zeros((S, E)), np.zeros(S, np.int64)
     live = np.zeros(T, bool)
