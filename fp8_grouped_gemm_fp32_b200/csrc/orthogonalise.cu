@@ -21,6 +21,10 @@
 // (a I + B_1)^2 A_1, all in s x s products, 3 s^2 l + 5 s^3 flops instead of 6 s^2 l + 2 s^3 (a fifth to a third
 // less for these two). A later pair must not: A_2 then carries A_1's rounding noise, grown by a^2, into directions
 // that the products with X would have resolved (2 to 3 times the error); in the first pair it does not show.
+//
+// Measured on a B200, 5 steps: four of 4096 x 2048 984 us (1.22 PFLOP/s, symmetric products counted half), 1167 us when
+// run on and on under the power cap (1.2 - 1.4 GHz): a K block takes 633 to 709 cycles, its MMAs 512. Sixteen of 256 x 512
+// 103 us: 15 products one after another at 7 us, most of it the way from a tile's release to the next one's first loads.
 #include <cmath>
 
 #include <algorithm>

@@ -20,6 +20,10 @@
 //     units a CTA (or pair); for dWg it leaves one partial tile per tile it touched, at index tile + its own index
 //     (unique: both only rise), and
 //  3. router_finish_kernel adds the partial tiles in order, and db. No float atomics: results repeat.
+//
+// Measured on a B200: 8192 x 7168 x 256 125 us replayed (383 MB; 120 GFLOP of MMAs, 104 us of it the products, where the
+// power cap takes the clock to 1.2 - 1.6 GHz), 4096 x 4096 x 64 34 us (products 28: dx's traffic, and filling two
+// pipelines), 5003 x 1408 x 100 30 us (latency of three launches), 256 x 512 x 8 4.8 us (one launch).
 #include <cmath>
 
 #include <algorithm>
