@@ -93,6 +93,8 @@ struct OrthoArgs {
     int mats;                // matrices of the wave
     int groups;
     int interleaved;
+    int square;              // single CTAs: symmetric products compute every tile (else those on and below the diagonal,
+                             // stored twice)
     int nsym0;               // symmetric products of the first group (1 or 5); the others have one
     OrthoSym sym0[kMostSym], sym;
     float ca0, ca;
@@ -121,7 +123,7 @@ struct OrthoShape {
         s = min(g.M, g.N);
         l = max(g.M, g.N);
         nb = (s + kEdge - 1) / kEdge;
-        ns = nb * (nb + 1) / 2;
+        ns = !PAIR && g.square ? nb * nb : nb * (nb + 1) / 2;
         rb = (g.M + kEdge - 1) / kEdge;
         cb = (g.N + kEdge - 1) / kEdge;
         nu = rb * cb;
@@ -161,6 +163,9 @@ struct OrthoWalk {
             // the shorter side runs fastest: neighbours share the longer operand's panel
             if (sh.tall) { t.ti = i / sh.cb; t.tj = i - t.ti * sh.cb; }
             else { t.tj = i / sh.rb; t.ti = i - t.tj * sh.rb; }
+        } else if (!PAIR && g.square) {
+            t.ti = i / sh.nb;
+            t.tj = i - t.ti * sh.nb;
         } else {
             int r = static_cast<int>((sqrtf(8.0f * i + 1.0f) - 1.0f) * 0.5f);
             while ((r + 1) * (r + 2) / 2 <= i) ++r;
@@ -347,7 +352,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
             const int rows = update ? g.M : sh.s, cols = update ? g.N : sh.s;
             const int cur = t.group & 1;
             const bool last = update && t.group == g.groups - 1;
-            const bool mirror = !update && t.ti != t.tj;
+            const bool mirror = !update && t.ti != t.tj && (PAIR || !g.square);
             // what comes in: X's two parts, or a symmetric product's addends
             const bool in0 = update || (t.kind == kSym && t.sym->u >= 0), in1 = update || (t.kind == kSym && t.sym->v >= 0);
             const float ca = t.group == 0 ? g.ca0 : g.ca, inv = 1.0f / kPScale;
@@ -1111,6 +1116,14 @@ int tiles_of(int M, int N) {
 // 1570 / 1061.
 bool use_pairs(int mats, int M, int N) { return static_cast<int64_t>(mats) * tiles_of<true>(M, N) >= 56; }
 
+// Where all tiles of a symmetric product run at once, storing a tile the second time, transposed, costs more than a CTA
+// that has nothing else to do computing it. Measured on a B200 (us, twice / all tiles): 256 x 512 92 / 85, 16 of them 104 /
+// 99, three of 1001 x 333 134 / 127, 1024 x 1024 152 / 145, 1024 x 2048 185 / 177.
+bool use_square(int mats, int side, int num_sms) {
+    const int nb = (side + 127) / 128;
+    return static_cast<int64_t>(mats) * nb * nb <= num_sms;
+}
+
 // The narrow kernel's CTAs all compute A, so a matrix of many of them only where all matrices run at once.
 int narrow_tiles(int M, int N) { return (std::max(M, N) + 127) / 128; }
 bool use_narrow(int mats, int M, int N) {
@@ -1296,6 +1309,8 @@ moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const v
         g.N = N;
         g.mats = std::min(wave, mats - m0);
         g.interleaved = interleaved;
+        const bool pairs = use_pairs(g.mats, M, N);
+        g.square = !pairs && use_square(g.mats, side, num_sms);
         // slots: 0 A, 1 Q; of two steps in one also 2 B_1, 3 B_1 A, 4 A_2, 5 B_2
         const float f = 1.0f / kPScale;
         const bool two = steps >= 2 && merges(M, N);
@@ -1327,7 +1342,7 @@ moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const v
         cudaError_t err = g_type == MOE_TYPE_FP32 ? launch_prepare<true>(gw, g.mats, g, w, eps, xscale, s)
                                                   : launch_prepare<false>(gw, g.mats, g, w, eps, xscale, s);
         if (err == cudaSuccess)
-            err = use_pairs(g.mats, M, N) ? launch_steps<true>(maps, g, num_sms, s) : launch_steps<false>(maps, g, num_sms, s);
+            err = pairs ? launch_steps<true>(maps, g, num_sms, s) : launch_steps<false>(maps, g, num_sms, s);
         if (err != cudaSuccess) return MOE_ERR_CUDA;
     }
     return MOE_OK;
