@@ -6,9 +6,10 @@
 // All of it is matrix products, and the tensor cores bound it: with s <= l the sides, a step is s^2 l (A: half
 // of a symmetric product) + s^3 (A^2, half) + 2 s^2 l flops. One persistent kernel runs every product of every
 // step: 256 x 256 tiles of CTA pairs (tcgen05 cta_group::2), or 128 x 128 tiles of single CTAs where there are
-// few; K blocks of 64 by TMA in a ring, two accumulators in tensor memory. A tile waits on its own matrix's counter only, so the matrices of a
-// batch fill each other's dependencies and the tail of one product overlaps the head of the next; symmetric
-// products compute the tiles on and below the diagonal and store each twice, the second time transposed.
+// few; K blocks of 64 by TMA in a ring, two accumulators in tensor memory. A tile waits on its own matrix's counter
+// only, so the matrices of a batch fill each other's dependencies and the tail of one product overlaps the head of the
+// next; symmetric products compute the tiles on and below the diagonal and store each twice, the second time transposed
+// (few tiles: all of them).
 //
 // Precision. Operands are fp16 (11 bits), sums fp32. The iteration multiplies X's small singular directions
 // by a, about 3.4, every step, and with them any rounding noise there: fp16 X alone ends up to 10 % off on
@@ -24,7 +25,9 @@
 //
 // Measured on a B200, 5 steps: four of 4096 x 2048 984 us (1.22 PFLOP/s, symmetric products counted half), 1167 us when
 // run on and on under the power cap (1.2 - 1.4 GHz): a K block takes 633 to 709 cycles, its MMAs 512. Sixteen of 256 x 512
-// 103 us: 15 products one after another at 7 us, most of it the way from a tile's release to the next one's first loads.
+// 99 us: 15 products one after another at 6.6 us (12,700 cycles), of which the MMAs of K = 512 at 32 KB a K block take
+// 4600, the epilogue 750 (A) to 2200 (update), its stores and their release 2500, the next tile's poll and first loads
+// the rest. Plain stores in place of the bulk stores are no faster (the release waits for them as long).
 #include <cmath>
 
 #include <algorithm>
@@ -500,24 +503,27 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                     for (int p = 0; p < 4; ++p) st_shared_v4(st0 + at(hp * 4 + p), o[p][0], o[p][1], o[p][2], o[p][3]);
                 }
                 if (last) {
-                    // rows leave 16 bytes a lane, eight lanes a row; sizes that are no multiple of 8 value by value
+                    // rows leave 16 bytes a lane, eight lanes a row; sizes that are no multiple of 8 by the value, 32 in a row
                     __syncwarp();
-                    const bool vec = g.N % 8 == 0;
+                    if (g.N % 8 == 0) {
 #pragma unroll 1
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = i * 4 + (lane >> 3), p = lane & 7;
-                        const int grow = row0 + r, gcol = col0 + p * 8;
-                        if (grow < rows && gcol < cols) {
-                            const uint4 u = ld_shared_v4(st0 + r * 128 + ((p ^ (r & 7)) << 4));
-                            uint16_t* dst = g.O + user_row(t.b, grow, g.M, g.interleaved) * g.N + gcol;
-                            if (vec) {
-                                *reinterpret_cast<uint4*>(dst) = u;
-                            } else {
-                                const uint32_t uu[4] = {u.x, u.y, u.z, u.w};
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = i * 4 + (lane >> 3), p = lane & 7;
+                            const int grow = row0 + r, gcol = col0 + p * 8;
+                            if (grow < rows && gcol < cols)
+                                *reinterpret_cast<uint4*>(g.O + user_row(t.b, grow, g.M, g.interleaved) * g.N + gcol) =
+                                    ld_shared_v4(st0 + r * 128 + ((p ^ (r & 7)) << 4));
+                        }
+                    } else {
+                        // the 32 rows lie one after another (a block of 128 is one matrix's)
+                        uint16_t* dst = g.O + user_row(t.b, row0, g.M, g.interleaved) * g.N + col0;
+                        const uint16_t* src = reinterpret_cast<const uint16_t*>(sm.stage[ew][0]);
+#pragma unroll 4
+                        for (int r = 0; r < 32; ++r) {
 #pragma unroll
-                                for (int c = 0; c < 8; ++c)
-                                    if (gcol + c < cols) dst[c] = static_cast<uint16_t>(uu[c >> 1] >> (16 * (c & 1)));
-                            }
+                            for (int c = lane; c < 64; c += 32)
+                                if (row0 + r < rows && col0 + c < cols)
+                                    dst[static_cast<int64_t>(r) * g.N + c] = src[r * 64 + (((c >> 3) ^ (r & 7)) << 3) + (c & 7)];
                         }
                     }
                     fence_proxy_async_smem();
@@ -578,16 +584,21 @@ int norm_blocks(int64_t n) {
     return static_cast<int>(std::min<int64_t>(kNormBlocks, (n + kNormThreads * kNormVals - 1) / (kNormThreads * kNormVals)));
 }
 
-// Place in the caller's array of value e of the wave's matrix m (offset from the wave's first matrix).
-__device__ __forceinline__ int64_t user_at(int64_t e, int m, int M, int N, int interleaved) {
+// Place in the caller's array of value e (below 2^28) of the wave's matrix m (offset from the wave's first matrix).
+__device__ __forceinline__ int64_t user_at(uint32_t e, int m, int M, int N, int interleaved) {
     if (!interleaved) return static_cast<int64_t>(m) * M * N + e;
-    const int64_t slab = static_cast<int64_t>(kGroup) * N;
-    return static_cast<int64_t>(m >> 1) * 2 * M * N + (e / slab * 2 + (m & 1)) * slab + e % slab;
+    const uint32_t slab = kGroup * static_cast<uint32_t>(N), q = e / slab;
+    return static_cast<int64_t>(m >> 1) * 2 * M * N + (2 * static_cast<int64_t>(q) + (m & 1)) * slab + (e - q * slab);
 }
 
-// Values e .. e + 7 of matrix m (n in all); VEC: aligned and whole.
+// A thread's eight values of matrix m (n in all) from a block's run of 2048: VEC (rows of whole 16-byte pieces): eight in
+// a row from e on, else every 256th.
+template <bool VEC>
+__device__ __forceinline__ uint32_t first_val(uint32_t run) {
+    return run * (kNormThreads * kNormVals) + threadIdx.x * (VEC ? kNormVals : 1);
+}
 template <bool F32, bool VEC>
-__device__ __forceinline__ void load_vals(const void* G, int64_t e, int64_t n, int m, int M, int N, int interleaved,
+__device__ __forceinline__ void load_vals(const void* G, uint32_t e, uint32_t n, int m, int M, int N, int interleaved,
                                           float (&v)[kNormVals]) {
     if constexpr (VEC) {
         const int64_t at = user_at(e, m, M, N, interleaved);
@@ -608,8 +619,8 @@ __device__ __forceinline__ void load_vals(const void* G, int64_t e, int64_t n, i
 #pragma unroll
         for (int i = 0; i < kNormVals; ++i) {
             v[i] = 0.0f;
-            if (e + i < n) {
-                const int64_t at = user_at(e + i, m, M, N, interleaved);
+            if (e + i * kNormThreads < n) {
+                const int64_t at = user_at(e + i * kNormThreads, m, M, N, interleaved);
                 v[i] = F32 ? static_cast<const float*>(G)[at] : bf16_bits_to_f32(static_cast<const uint16_t*>(G)[at]);
             }
         }
@@ -634,13 +645,12 @@ ortho_norm_kernel(const void* __restrict__ G, int M, int N, int interleaved, dou
                   unsigned* __restrict__ done) {
     __shared__ double scratch[kNormThreads / 32];
     const int m = blockIdx.y;
-    const int64_t n = static_cast<int64_t>(M) * N;
+    const uint32_t n = static_cast<uint32_t>(M) * N;
     dependents_may_launch();
     wait_for_producers();
     if (blockIdx.x == 0 && threadIdx.x == 0) done[m * kDoneStride] = 0;
     double s = 0.0;
-    for (int64_t e = (static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x) * kNormVals; e < n;
-         e += static_cast<int64_t>(gridDim.x) * kNormThreads * kNormVals) {
+    for (uint32_t run = blockIdx.x, e; (e = first_val<VEC>(run)) < n; run += gridDim.x) {
         float v[kNormVals];
         load_vals<F32, VEC>(G, e, n, m, M, N, interleaved, v);
 #pragma unroll
@@ -656,15 +666,14 @@ ortho_convert_kernel(const void* __restrict__ G, int M, int N, int ldx, int inte
                      double eps, double xscale, uint16_t* __restrict__ hi, uint16_t* __restrict__ lo) {
     __shared__ double scratch[kNormThreads / 32];
     const int m = blockIdx.y;
-    const int64_t n = static_cast<int64_t>(M) * N;
+    const uint32_t n = static_cast<uint32_t>(M) * N;
     wait_for_producers();
     double s = 0.0;
     for (int i = threadIdx.x; i < static_cast<int>(gridDim.x); i += kNormThreads) s += part[static_cast<int64_t>(m) * gridDim.x + i];
     s = block_sum_f64(s, scratch);
     const double inv = xscale / (sqrt(s) + eps);
     const int64_t base = static_cast<int64_t>(m) * M * ldx;
-    for (int64_t e = (static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x) * kNormVals; e < n;
-         e += static_cast<int64_t>(gridDim.x) * kNormThreads * kNormVals) {
+    for (uint32_t run = blockIdx.x, e; (e = first_val<VEC>(run)) < n; run += gridDim.x) {
         float v[kNormVals];
         load_vals<F32, VEC>(G, e, n, m, M, N, interleaved, v);
         alignas(16) uint16_t h[kNormVals], r[kNormVals];
@@ -682,8 +691,9 @@ ortho_convert_kernel(const void* __restrict__ G, int M, int N, int ldx, int inte
         } else {
 #pragma unroll
             for (int i = 0; i < kNormVals; ++i)
-                if (e + i < n) {
-                    const int64_t at = base + (e + i) / N * ldx + (e + i) % N;
+                if (e + i * kNormThreads < n) {
+                    const uint32_t row = (e + i * kNormThreads) / N, col = e + i * kNormThreads - row * N;
+                    const int64_t at = base + static_cast<int64_t>(row) * ldx + col;
                     hi[at] = h[i];
                     lo[at] = r[i];
                 }
