@@ -23,9 +23,9 @@
 // less for these two). A later pair must not: A_2 then carries A_1's rounding noise, grown by a^2, into directions
 // that the products with X would have resolved (2 to 3 times the error); in the first pair it does not show.
 //
-// Measured on a B200, 5 steps: four of 4096 x 2048 984 us (1.22 PFLOP/s, symmetric products counted half), 1167 us when
+// Measured on a B200, 5 steps: four of 4096 x 2048 984 us (1.22 PFLOP/s, symmetric products counted half), 1186 us when
 // run on and on under the power cap (1.2 - 1.4 GHz): a K block takes 633 to 709 cycles, its MMAs 512. Sixteen of 256 x 512
-// 99 us: 15 products one after another at 6.6 us (12,700 cycles), of which the MMAs of K = 512 at 32 KB a K block take
+// 97 us: 15 products one after another at 6.6 us (12,700 cycles), of which the MMAs of K = 512 at 32 KB a K block take
 // 4600, the epilogue 750 (A) to 2200 (update), its stores and their release 2500, the next tile's poll and first loads
 // the rest. Plain stores in place of the bulk stores are no faster (the release waits for them as long).
 #include <cmath>
