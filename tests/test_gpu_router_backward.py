@@ -159,3 +159,27 @@ def test_gradient_against_differences():
         d = torch.zeros_like(b)
         d[e] = 0.5
         assert abs(loss(x, W, b + d) - loss(x, W, b - d) - float(db[e])) <= 16 * U * float(c.dl[:, e].abs().sum()) + 1e-9
+
+
+@pytest.mark.parametrize("T,E", [(300, 16), (900, 70), (900, 140)])
+def test_two_at_once_and_captured_behind_a_memset_and_a_copy(T, E):
+    cases = [Case(T, 640, E), Case(T + 31, 640, E)]
+    want = [[t.clone() for t in c.run().outputs()] for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(3):                                     # each on its own stream, with its own workspace
+        for c, s in zip(cases, streams):
+            c.run(s)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert all(torch.equal(x, y) for x, y in zip(w, c.outputs()))
+    c, src, s = cases[0], cases[0].dl.clone(), torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        c.ws.zero_()
+        c.dl.copy_(src)
+        c.run()
+    c.dl.fill_(7)
+    g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(want[0], c.outputs()))
