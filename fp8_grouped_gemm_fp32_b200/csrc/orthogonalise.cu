@@ -53,6 +53,12 @@ constexpr int kOOper = 2 * kOBox;            // a CTA's 128 rows of an operand
 // barrier is not reused before it was waited for.
 constexpr int kOReady = 16;
 static_assert(kOReady > kOStages + 3, "a tile's barrier must outlast the tiles in flight");
+// "Every epilogue warp has stored its part of a tile", a barrier a counted tile in turn. Only the counting warp waits for
+// it, so another may be ahead: of a slow warp at tile n (accumulator released, box not stored) by two tiles at most, since
+// tile n + 3's accumulator is computed once every warp has released that of n + 1. One barrier would take a quick
+// warp's arrivals of n + 1 and n + 2 for the slow one's and count n while its box is not in memory.
+constexpr int kOStored = 4;
+static_assert(kOStored >= 3, "a warp may be two tiles ahead of another");
 constexpr int kOThreads = 384;               // TMA, MMA, two idle warps, eight epilogue warps
 constexpr int kOEpi = 8;
 constexpr float kPScale = 64.0f;             // A and B are stored times this
@@ -68,7 +74,7 @@ struct SmemO {
     uint64_t tfull[2];
     uint64_t tempty[2];
     uint64_t eload[kOEpi];
-    uint64_t stored;
+    uint64_t stored[kOStored];
     uint64_t ready[kOReady];
     uint32_t tmem_base;
     volatile int abort_flag;
@@ -229,7 +235,7 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
             mbar_init(&sm.tempty[i], (PAIR ? 2 : 1) * kOEpi);
         }
         for (int i = 0; i < kOEpi; ++i) mbar_init(&sm.eload[i], 1);
-        mbar_init(&sm.stored, kOEpi);
+        for (int i = 0; i < kOStored; ++i) mbar_init(&sm.stored[i], kOEpi);
         for (int i = 0; i < kOReady; ++i) mbar_init(&sm.ready[i], 1);
         sm.abort_flag = 0;
         fence_mbar_init();
@@ -548,9 +554,9 @@ ortho_steps_kernel(const __grid_constant__ OrthoMaps maps, const __grid_constant
                 int good = 1;
                 if (lane == 0) {
                     bulk_wait_all();
-                    mbar_arrive(&sm.stored);
+                    mbar_arrive(&sm.stored[tiles % kOStored]);
                     if (ew == 0) {
-                        good = mbar_wait(&sm.stored, tiles & 1, kOrthoWaitNs);
+                        good = mbar_wait(&sm.stored[tiles % kOStored], (tiles / kOStored) & 1, kOrthoWaitNs);
                         if (good) add_release_gpu(g.done + t.b * kDoneStride, 1);
                     }
                 }

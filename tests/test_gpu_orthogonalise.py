@@ -212,3 +212,21 @@ def test_two_graphs_with_their_own_workspaces_at_once():
                 g.replay()
     done(outs[0])
     assert all(torch.equal(o, w) for o, w in zip(outs, wants))
+
+
+@pytest.mark.parametrize("batch,M,N", [(3, 1000, 900), (12, 600, 700), (6, 1100, 1100), (4, 1536, 1024)])
+def test_several_tiles_a_cta_of_several_matrices_repeat_and_equal_each_alone(batch, M, N):
+    # a CTA goes from one matrix's last tile of a product to the next matrix's, which must not count the first early
+    G = torch.stack([ortho_matrix(M, N, "decay", i) for i in range(batch)]).to(torch.bfloat16).cuda()
+    ws = torch.empty(api.moe_orthogonalise_workspace_size(batch, M, N), dtype=torch.uint8, device="cuda")
+    alone = torch.cat([done(run(G[i:i + 1].contiguous(), 1, M, N)) for i in range(batch)])
+    want = done(run(G, batch, M, N, ws=ws))
+    if min(M, N) >= 1024 and 2 * max(M, N) >= 3 * min(M, N):
+        # The first two steps at once hold B_1 A, symmetric up to rounding only: (i, j) sums B_1[i, k] A[k, j], (j, i) sums
+        # B_1[j, k] A[k, i], other products. A few tiles are all computed, many computed once and mirrored: other bits.
+        for i in range(batch):
+            assert ref.rel_norm(want[i], ref.orthogonalise(G[i])) <= 2.0 ** -8 + 2.0 ** -8
+    else:
+        assert torch.equal(want, alone)
+    for _ in range(20):
+        assert torch.equal(done(run(G, batch, M, N, ws=ws)), want)
