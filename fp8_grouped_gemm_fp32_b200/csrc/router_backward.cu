@@ -5,12 +5,11 @@
 // about the same, so both products run on the tensor cores and dx is bound by its own traffic.
 //
 //  1. Preparation. dl goes into three bf16 parts (8 + 8 + 8 bits, all of fp32) for dWg, with partial column sums for
-//     db. For dx, up to 128 experts W_g goes into two bf16 parts and dx = d1 w1 + d1 w2 + d2 w1 (error 2^-15; three
-//     products of so few experts hide behind dx's traffic, and nothing has to be known before the parts are made:
-//     one launch). Above, one product has to do: fp16 copies, 11 bits, off by an eighth of the step dx is rounded
-//     with; each expert's W_g row scaled by a power of two so that its largest entry lies in [512, 1024), that power
-//     moved into dl, then each token's dl row scaled likewise (undone in dx's epilogue).
-//  2. router_products_kernel, dx: a CTA keeps its W_g panel (all experts x 256 columns) in shared memory and
+//     db. W_g goes into two, and dx = d1 w1 + d1 w2 + d2 w1: off by 2^-18 of a term or three. Fewer bits would show:
+//     rows of a softmax's gradient sum to zero, so what W_g's rows share cancels while its rounding errors do not (a
+//     shared row of 100 times their spread: fp16 operands leave dx 2.6e-2 off, these 4e-4, its own rounding is 1.7e-3).
+//     bf16 needs no scales: nothing has to be known before the parts are made, so this is one launch.
+//  2. router_products_kernel, dx: a CTA keeps its W_g panel (all experts x 256 or 128 columns) in shared memory and
 //     streams token tiles through it (without that the panels alone would cost more L2 traffic than dx does HBM
 //     traffic), the next box of dx0 loading meanwhile. dWg: the transposed product, x^T (rows h) by the parts of
 //     dl, both operands read as they lie in memory (MN-major), so E is the MMA's N and a few experts cost little:
@@ -21,14 +20,10 @@
 //     (unique: both only rise), and
 //  3. router_finish_kernel adds the partial tiles in order, and db. No float atomics: results repeat.
 //
-// Measured on a B200: 8192 x 7168 x 256 125 us replayed (383 MB; 120 GFLOP of MMAs, 104 us of it the products, where the
-// power cap takes the clock to 1.2 - 1.6 GHz), 4096 x 4096 x 64 34 us (products 28: dx's traffic, and filling two
+// Measured on a B200: 8192 x 7168 x 256 188 us a call among others (383 MB; 180 GFLOP of MMAs, where the power cap takes
+// the clock to 1.2 - 1.6 GHz; 150 us with one fp16 product for dx, which lost the bits named above), 4096 x 4096 x 64 34 us (products 28: dx's traffic, and filling two
 // pipelines), 5003 x 1408 x 100 30 us (latency of three launches), 256 x 512 x 8 4.8 us (one launch).
-#include <cmath>
-
 #include <algorithm>
-
-#include <cuda_fp16.h>
 
 #include "../../include/moe_fp8.h"
 #include "common.cuh"
@@ -47,46 +42,11 @@ constexpr int kRbChunk = 128;                  // tokens summed in tensor memory
 
 __device__ __forceinline__ uint16_t bf16_bits(float f) { return __bfloat16_as_ushort(__float2bfloat16_rn(f)); }
 
-// 2^(9 - exponent of m), so that m times it lies in [512, 1024), and its inverse; 1 for m = 0, infinite or NaN.
-__device__ __forceinline__ float2 pow2_scale(float m) {
-    if (!(m > 0.0f) || m > 3.0e38f) return make_float2(1.0f, 1.0f);
-    const int e = min(max(9 - ilogbf(m), -100), 100);
-    return make_float2(exp2f(static_cast<float>(e)), exp2f(static_cast<float>(-e)));
-}
-
 // ---------------------------------------------------------------- 1. preparation
-// Above 128 experts: W_g row e -> fp16, scaled; wscale[e] = the inverse of the scale.
-__global__ void __launch_bounds__(256)
-router_prep_w_kernel(const float* __restrict__ Wg, int H, uint16_t* __restrict__ wh, float* __restrict__ wscale) {
-    __shared__ float sm[8];
-    const int64_t base = static_cast<int64_t>(blockIdx.x) * H;
-    dependents_may_launch();
-    wait_for_producers();
-    float m = 0.0f;
-#pragma unroll 4
-    for (int h = threadIdx.x * 4; h < H; h += 1024) {
-        const float4 f = *reinterpret_cast<const float4*>(Wg + base + h);
-        m = fmaxf(m, fmaxf(fmaxf(fabsf(f.x), fabsf(f.y)), fmaxf(fabsf(f.z), fabsf(f.w))));
-    }
-    m = warp_max(m);
-    if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, sm[i]);
-    const float2 sc = pow2_scale(m);
-    if (threadIdx.x == 0) wscale[blockIdx.x] = sc.y;
-#pragma unroll 4
-    for (int h = threadIdx.x * 4; h < H; h += 1024) {
-        const float4 f = *reinterpret_cast<const float4*>(Wg + base + h);
-        const __half2 a = __floats2half2_rn(f.x * sc.x, f.y * sc.x), b = __floats2half2_rn(f.z * sc.x, f.w * sc.x);
-        *reinterpret_cast<uint2*>(wh + base + h) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    }
-}
-
-// Up to 128 experts. The first dl_blocks blocks: dl rows -> three bf16 parts side by side, [T][3][pitch] with zeros
-// behind the last expert, and the block's column sums; a warp takes a token at a time, four experts a lane. The
-// others: W_g -> two bf16 parts [2][E][H], 4096 values a block.
+// The first dl_blocks blocks: dl rows -> three bf16 parts and the block's column sums; a warp takes a token at a time, Q
+// groups of four experts a lane (16-byte reads where E is a multiple of 4). Value e of part p of token t goes to
+// t * row + p * part + e, with zeros behind the last expert up to `width`. The others: W_g -> two bf16 parts [2][E][H],
+// 4096 values a block.
 constexpr int kPrepW = 4096;
 
 // The first part holds an infinite or NaN value alone; what is left of a finite one is exact.
@@ -95,11 +55,12 @@ __device__ __forceinline__ void put4(uint16_t* dst, const uint16_t (&u)[4]) {
     *reinterpret_cast<uint2*>(dst) = make_uint2(u[0] | static_cast<uint32_t>(u[1]) << 16, u[2] | static_cast<uint32_t>(u[3]) << 16);
 }
 
-template <bool VEC>
+template <int Q, bool VEC>
 __global__ void __launch_bounds__(256)
-router_prep_parts_kernel(const float* __restrict__ dl, const float* __restrict__ Wg, int T, int H, int E, int pitch,
-                         int dl_blocks, uint16_t* __restrict__ parts, float* __restrict__ dbpart, uint16_t* __restrict__ w2) {
-    __shared__ float sm[8][128];
+router_prep_parts_kernel(const float* __restrict__ dl, const float* __restrict__ Wg, int T, int H, int E, int width,
+                         int64_t row, int64_t part, int dl_blocks, uint16_t* __restrict__ parts,
+                         float* __restrict__ dbpart, uint16_t* __restrict__ w2) {
+    __shared__ float sm[8][Q * 128];
     dependents_may_launch();
     wait_for_producers();
     if (static_cast<int>(blockIdx.x) >= dl_blocks) {
@@ -123,124 +84,48 @@ router_prep_parts_kernel(const float* __restrict__ dl, const float* __restrict__
             }
         return;
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = 4 * lane;
-    const int t0 = blockIdx.x * kPrepTokens + warp;
-    float v[kPrepTokens / 8][4], sum[4] = {};
-#pragma unroll
-    for (int k = 0; k < kPrepTokens / 8; ++k) {
-        const int t = t0 + 8 * k;
-        const float* p = dl + static_cast<int64_t>(t) * E + e;
-        if constexpr (VEC) {
-            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (t < T && e < E) f = *reinterpret_cast<const float4*>(p);
-            v[k][0] = f.x; v[k][1] = f.y; v[k][2] = f.z; v[k][3] = f.w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[k][i] = t < T && e + i < E ? p[i] : 0.0f;
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < kPrepTokens / 8; ++k) {
-        const int t = t0 + 8 * k;
-        uint16_t b[3][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            sum[i] += v[k][i];
-            float r = v[k][i];
-#pragma unroll
-            for (int p = 0; p < 3; ++p) {
-                b[p][i] = bf16_bits(r);
-                r = rest_of(r, b[p][i]);
-            }
-        }
-        if (t < T && e < pitch) {
-#pragma unroll
-            for (int p = 0; p < 3; ++p) put4(parts + (static_cast<int64_t>(t) * 3 + p) * pitch + e, b[p]);
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) sm[warp][e + i] = sum[i];
-    __syncthreads();
-    if (threadIdx.x < E) {
-        float s = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s += sm[i][threadIdx.x];
-        dbpart[static_cast<int64_t>(blockIdx.x) * E + threadIdx.x] = s;
-    }
-}
-
-// Above 128 experts. dl rows -> fp16 (times the experts' inverse scales, then scaled per token; tscale[t] undoes it), three bf16
-// parts [3][T][ld], and the block's column sums. A warp takes a token at a time; Q groups of four experts a lane
-// (16-byte reads where E is a multiple of 4).
-template <int Q, bool VEC>
-__global__ void __launch_bounds__(256)
-router_prep_dl_kernel(const float* __restrict__ dl, const float* __restrict__ wscale, int T, int E, int ld,
-                      uint16_t* __restrict__ dlh, float* __restrict__ tscale, uint16_t* __restrict__ parts,
-                      float* __restrict__ dbpart) {
-    __shared__ float sm[8][Q * 128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int t0 = blockIdx.x * kPrepTokens + warp, t1 = min((static_cast<int>(blockIdx.x) + 1) * kPrepTokens, T);
-    const int64_t plane = static_cast<int64_t>(T) * ld;
-    auto load = [&](int t, float (&v)[4 * Q]) {
+    const int t0 = blockIdx.x * kPrepTokens + warp;
+    float v[kPrepTokens / 8][4 * Q], sum[4 * Q] = {};
+#pragma unroll
+    for (int k = 0; k < kPrepTokens / 8; ++k) {
+        const int t = t0 + 8 * k;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int e = 4 * (lane + 32 * q);
             const float* p = dl + static_cast<int64_t>(t) * E + e;
             if constexpr (VEC) {
                 float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (t < t1 && e < E) f = *reinterpret_cast<const float4*>(p);
-                v[4 * q] = f.x; v[4 * q + 1] = f.y; v[4 * q + 2] = f.z; v[4 * q + 3] = f.w;
+                if (t < T && e < E) f = *reinterpret_cast<const float4*>(p);
+                v[k][4 * q] = f.x; v[k][4 * q + 1] = f.y; v[k][4 * q + 2] = f.z; v[k][4 * q + 3] = f.w;
             } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[4 * q + i] = t < t1 && e + i < E ? p[i] : 0.0f;
+                for (int i = 0; i < 4; ++i) v[k][4 * q + i] = t < T && e + i < E ? p[i] : 0.0f;
             }
         }
-    };
-    dependents_may_launch();
-    wait_for_producers();
-    float v[4 * Q], sum[4 * Q], w[4 * Q];
-    load(t0, v);
-#pragma unroll
-    for (int i = 0; i < 4 * Q; ++i) {
-        const int e = 4 * (lane + 32 * (i / 4)) + i % 4;
-        sum[i] = 0.0f;
-        w[i] = e < E ? wscale[e] : 0.0f;
     }
-    for (int t = t0; t < t1; t += 8) {
-        float nx[4 * Q];
-        load(t + 8, nx);
-        float m = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4 * Q; ++i) {
-            sum[i] += v[i];
-            m = fmaxf(m, fabsf(v[i] * w[i]));
-        }
-        const float2 sc = pow2_scale(warp_max(m));
-        if (lane == 0) tscale[t] = sc.y;
+    for (int k = 0; k < kPrepTokens / 8; ++k) {
+        const int t = t0 + 8 * k;
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int e = 4 * (lane + 32 * q);
-            if (e < E) {
-                // rows are padded to a multiple of 8 experts: whole 8-byte stores, zeros behind the last
-                const int64_t at = static_cast<int64_t>(t) * ld + e;
-                uint16_t h[4], b[3][4];
+            uint16_t b[3][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    h[i] = __half_as_ushort(__float2half_rn(v[4 * q + i] * w[4 * q + i] * sc.x));
-                    float r = v[4 * q + i];
+            for (int i = 0; i < 4; ++i) {
+                float r = v[k][4 * q + i];
+                sum[4 * q + i] += r;
 #pragma unroll
-                    for (int p = 0; p < 3; ++p) {
-                        b[p][i] = bf16_bits(r);
-                        r = rest_of(r, b[p][i]);
-                    }
+                for (int p = 0; p < 3; ++p) {
+                    b[p][i] = bf16_bits(r);
+                    r = rest_of(r, b[p][i]);
                 }
-                put4(dlh + at, h);
+            }
+            if (t < T && e < width) {
 #pragma unroll
-                for (int p = 0; p < 3; ++p) put4(parts + p * plane + at, b[p]);
+                for (int p = 0; p < 3; ++p) put4(parts + t * row + p * part + e, b[p]);
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4 * Q; ++i) v[i] = nx[i];
     }
 #pragma unroll
     for (int i = 0; i < 4 * Q; ++i) sm[warp][4 * (lane + 32 * (i / 4)) + i % 4] = sum[i];
@@ -254,20 +139,21 @@ router_prep_dl_kernel(const float* __restrict__ dl, const float* __restrict__ ws
 }
 
 // ---------------------------------------------------------------- 2. the products
-// PAIR (above 128 experts): CTA pairs, 256 tokens x 256 columns of dx, 256 columns x 256 experts of dWg. The
+// PAIR (above 128 experts): CTA pairs, 256 tokens x `kPanel` columns of dx, 256 columns x 256 experts of dWg. The
 // operand that both halves of a tile need is then held once a pair: 64 KB a stage cross from L2 where single CTAs
 // would load 112 KB for the same MMAs. Otherwise single CTAs, 128 x 256 and 128 x `pitch` (16, 32, 64 or 128). KB:
-// 64-expert blocks of the W_g panel (of both its parts), AS: those of the tokens' ring, NB: dx0 / dx boxes an epilogue
-// warp holds (what the panel leaves room for).
+// 64-expert blocks of the W_g panel, of both its parts in turn; WB: 64-column boxes of one that a CTA holds; AS: blocks of
+// the tokens' ring, NB: dx0 / dx boxes an epilogue warp holds (what the panel leaves room for). The panel is 256 columns
+// wide, above 256 experts 128.
 // Units are dealt out as runs: group g of G takes [g U / G, (g + 1) U / G).
 constexpr int kDwStages = 4;                                               // barriers; the ring's depth goes by E
 constexpr int kDwRing = 24 * kRbBox;                                       // its bytes: 192 KB
 constexpr int kDwRegsLow = 40, kDwRegsHigh = 232;                          // as in the grouped GEMM:
 constexpr int kDwRegsSplit = 128 * kDwRegsLow + 256 * kDwRegsHigh;        // what the launch must have allocated
 
-template <bool PAIR, int KB, int AS, int NB>
+template <int KB, int WB, int AS, int NB>
 struct SmemDx {
-    uint8_t w[KB][PAIR ? 2 * kRbBox : 4 * kRbBox];     // the CTA's 128 (of a pair's 256) or 256 panel columns
+    uint8_t w[KB][WB * kRbBox];                        // the CTA's panel columns (of a pair's half of them)
     uint8_t a[AS][2 * kRbBox];                         // 64 experts of 128 tokens
     uint8_t stage[8][NB][4096];                        // per epilogue warp: 32 rows x 64 columns, bf16
 };
@@ -277,10 +163,10 @@ struct SmemDx {
 struct SmemDw {
     uint8_t ring[kDwRing];
 };
-template <bool PAIR, int KB, int AS, int NB>
+template <int KB, int WB, int AS, int NB>
 struct SmemP {
     union {
-        SmemDx<PAIR, KB, AS, NB> dx;
+        SmemDx<KB, WB, AS, NB> dx;
         SmemDw dw;
     };
     uint64_t wfull, wempty;
@@ -303,12 +189,11 @@ struct RouterArgs {
     int etiles;               // expert tiles of dWg
     int pitch;                // single CTAs: columns of a part of dl, its experts rounded up
     int Ux, Uw;
-    const float* tscale;
     float* part;
     int* status;
 };
 
-template <bool PAIR, int KB, int AS, int NB>
+template <bool PAIR, int KB, int WB, int AS, int NB>
 __global__ void __launch_bounds__(kRbThreads, 1)
 router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_constant__ CUtensorMap tm_w,
                        const __grid_constant__ CUtensorMap tm_in, const __grid_constant__ CUtensorMap tm_out,
@@ -316,9 +201,9 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                        const RouterArgs g) {
     constexpr int kTok = PAIR ? 256 : 128;                      // tokens of a dx tile
     constexpr int kRows = PAIR ? 256 : 128, kCols = PAIR ? 256 : 128;   // dWg tile: columns of x, experts
-    constexpr int kWBoxes = PAIR ? 2 : 4;                       // 64-column boxes of the panel this CTA holds
+    constexpr int kPanel = (PAIR ? 2 : 1) * 64 * WB, kBoxes = kPanel / 128;     // its boxes of a unit, an epilogue warp
     extern __shared__ uint8_t smem_raw[];
-    using SP = SmemP<PAIR, KB, AS, NB>;
+    using SP = SmemP<KB, WB, AS, NB>;
     SP& sm = *reinterpret_cast<SP*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = PAIR ? cluster_ctarank() : 0;
@@ -397,25 +282,24 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                             if (panels > 0 && !mbar_wait(&sm.wempty, (panels - 1) & 1, kRbWaitNs)) { fail(); break; }
                             have = panel;
                             ++panels;
-                            const int c0 = panel * 256 + static_cast<int>(rank) * 128;
-                            // PAIR: this CTA's half of the panel; else both parts of all of it
-                            const int blocks = PAIR ? kblocks : 2 * kblocks;
-                            if (rank == 0) mbar_arrive_expect_tx(&sm.wfull, (PAIR ? 2u : 1u) * blocks * kWBoxes * kRbBox);
-                            for (int kb = 0; kb < blocks; ++kb)
-                                for (int i = 0; i < kWBoxes; ++i) {
+                            const int c0 = panel * kPanel + static_cast<int>(rank) * 64 * WB;
+                            // both parts of the panel (PAIR: of this CTA's half of it)
+                            if (rank == 0) mbar_arrive_expect_tx(&sm.wfull, (PAIR ? 2u : 1u) * 2 * kblocks * WB * kRbBox);
+                            for (int kb = 0; kb < 2 * kblocks; ++kb)
+                                for (int i = 0; i < WB; ++i) {
                                     if constexpr (PAIR)
-                                        tma_load_3d_pair(sm.dx.w[kb] + i * kRbBox, &tm_w, leader_bar(&sm.wfull), c0 + 64 * i, kb * 64, 0);
+                                        tma_load_3d_pair(sm.dx.w[kb] + i * kRbBox, &tm_w, leader_bar(&sm.wfull), c0 + 64 * i, (kb >> 1) * 64, kb & 1);
                                     else
                                         tma_load_3d(sm.dx.w[kb] + i * kRbBox, &tm_w, &sm.wfull, c0 + 64 * i, (kb >> 1) * 64, kb & 1);
                                 }
                         }
-                        // PAIR: the tile's fp16 dl; else its first part and its second, block by block
-                        for (int kb = 0; kb < (PAIR ? kblocks : 2 * kblocks); ++kb, ++it) {
+                        // the tile's dl, its first part and its second, block by block
+                        for (int kb = 0; kb < 2 * kblocks; ++kb, ++it) {
                             const int s = it % AS;
                             if (!mbar_wait(&sm.aempty[s], ((it / AS) & 1) ^ 1, kRbWaitNs)) { fail(); ok = false; break; }
                             if (rank == 0) mbar_arrive_expect_tx(&sm.afull[s], (PAIR ? 2u : 1u) * 2 * kRbBox);
                             if constexpr (PAIR)
-                                tma_load_2d_pair(sm.dx.a[s], &tm_dl, leader_bar(&sm.afull[s]), kb * 64, tile * kTok + static_cast<int>(rank) * 128);
+                                tma_load_3d_pair(sm.dx.a[s], &tm_dl, leader_bar(&sm.afull[s]), (kb >> 1) * 64, tile * kTok + static_cast<int>(rank) * 128, kb & 1);
                             else
                                 tma_load_2d(sm.dx.a[s], &tm_dl, &sm.afull[s], (kb & 1) * g.pitch + (kb >> 1) * 64, tile * kTok);
                         }
@@ -423,7 +307,7 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                 } else if (warp == 1 && lane == 0 && rank == 0) {
                     uint32_t it = 0, ti = 0, panels = 0;
                     int have = -1;
-                    const uint32_t idesc = f16_idesc(kTok, 256, !PAIR, false, true);
+                    const uint32_t idesc = f16_idesc(kTok, kPanel, true, false, true);
                     bool ok = !sm.abort_flag;
                     for (int u = x0; ok && u < x1 && !sm.abort_flag; ++u, ++ti) {
                         const int panel = u / ttiles;
@@ -435,22 +319,25 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                         const uint32_t buf = ti & 1, d = tmem + buf * 256;
                         if (!mbar_wait(&sm.tempty[0][buf], ((ti >> 1) & 1) ^ 1, kRbWaitNs)) { fail(); break; }
                         tc_fence_after();
-                        for (int kb = 0; kb < (PAIR ? kblocks : 2 * kblocks); ++kb, ++it) {
+                        for (int kb = 0; kb < 2 * kblocks; ++kb, ++it) {
                             const int s = it % AS;
                             if (!mbar_wait(&sm.afull[s], (it / AS) & 1, kRbWaitNs)) { fail(); ok = false; break; }
                             tc_fence_after();
                             // 16 experts on (the descriptors hold address / 16): 32 bytes in a row, 2048 in the panel
                             const uint64_t da = sw128_kmajor_desc(smem_u32(sm.dx.a[s]));
-                            const uint64_t db = sw128_mnmajor_desc(smem_u32(sm.dx.w[PAIR ? kb : kb & ~1]), kRbBox);
+                            const uint64_t db = sw128_mnmajor_desc(smem_u32(sm.dx.w[kb & ~1]), kRbBox);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk) {
                                 if constexpr (PAIR) umma_f16_pair(d, da + kk * 2, db + kk * 128, idesc, kb + kk > 0);
                                 else umma_f16(d, da + kk * 2, db + kk * 128, idesc, kb + kk > 0);
                             }
-                            if (!PAIR && !(kb & 1)) {              // the first part of dl also meets the second of W_g
+                            if (!(kb & 1)) {                       // the first part of dl also meets the second of W_g
                                 const uint64_t d2 = sw128_mnmajor_desc(smem_u32(sm.dx.w[kb | 1]), kRbBox);
 #pragma unroll
-                                for (int kk = 0; kk < 4; ++kk) umma_f16(d, da + kk * 2, d2 + kk * 128, idesc, 1);
+                                for (int kk = 0; kk < 4; ++kk) {
+                                    if constexpr (PAIR) umma_f16_pair(d, da + kk * 2, d2 + kk * 128, idesc, 1);
+                                    else umma_f16(d, da + kk * 2, d2 + kk * 128, idesc, 1);
+                                }
                             }
                             if constexpr (PAIR) umma_commit_pair(&sm.aempty[s], 0x3); else umma_commit(&sm.aempty[s]);
                         }
@@ -527,14 +414,14 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
         for (int turn = 0; turn < 2; ++turn) {
             if (turn == dx_turn) {
                 const int ew = warp - 4, q = warp & 3, half = ew >> 2;
-                // the warp's 32 rows x 128 columns of a unit as two boxes of 64 columns; box j goes through buffer
+                // the warp's 32 rows x half a panel of a unit as kBoxes boxes of 64 columns; box j goes through buffer
                 // j % NB: dx0 comes in one box ahead, dx leaves from the same place
-                const uint32_t boxes = static_cast<uint32_t>(2 * (x1 - x0));
+                const uint32_t boxes = static_cast<uint32_t>(kBoxes * (x1 - x0));
                 auto place = [&](uint32_t j, int& row0, int& col0) {
-                    const int u = x0 + static_cast<int>(j >> 1);
+                    const int u = x0 + static_cast<int>(j / kBoxes);
                     const int panel = u / ttiles, tile = u - panel * ttiles;
                     row0 = tile * kTok + static_cast<int>(rank) * 128 + q * 32;
-                    col0 = panel * 256 + half * 128 + 64 * static_cast<int>(j & 1);
+                    col0 = panel * kPanel + half * (kPanel / 2) + 64 * static_cast<int>(j % kBoxes);
                 };
                 auto fetch = [&](uint32_t j) {         // lane 0
                     int row0, col0;
@@ -544,24 +431,22 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                     tma_load_2d(sm.dx.stage[ew][j % NB], &tm_in, bar, col0, row0);
                 };
                 if (g.has_base && lane == 0 && boxes > 0 && !sm.abort_flag) fetch(0);
-                float sc = 1.0f;                       // undoes the token's scale
                 for (uint32_t j = 0; j < boxes; ++j) {
                     if (sm.abort_flag) break;
-                    const uint32_t ti = j >> 1, buf = ti & 1, n = j % NB;
+                    const uint32_t ti = j / kBoxes, buf = ti & 1, n = j % NB;
                     int row0, col0;
                     place(j, row0, col0);
-                    if (PAIR && !(j & 1)) sc = row0 + lane < g.T ? g.tscale[row0 + lane] : 0.0f;
                     if (lane == 0) {
                         bulk_wait_read<NB - 2>();      // box j + 1 - NB has left the buffer that box j + 1 goes to
                         if (g.has_base && j + 1 < boxes) fetch(j + 1);
                     }
                     __syncwarp();
-                    if (!(j & 1)) {
+                    if (j % kBoxes == 0) {
                         if (!mbar_wait(&sm.tfull[0][buf], (ti >> 1) & 1, kRbWaitNs)) { fail(); break; }
                         tc_fence_after();
                     }
                     if (g.has_base && !mbar_wait(&sm.eload[ew][n], (j / NB) & 1, kRbWaitNs)) { fail(); break; }
-                    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * 128 + 64 * (j & 1);
+                    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + buf * 256 + half * (kPanel / 2) + 64 * (j % kBoxes);
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {      // 32 columns at a time
                         float v[32];
@@ -576,7 +461,7 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                                 asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(b[p][0]), "=r"(b[p][1]), "=r"(b[p][2]), "=r"(b[p][3]) : "r"(at(p)) : "memory");
                         }
                         tmem_ld_wait();
-                        if (i == 1 && (j & 1)) {
+                        if (i == 1 && j % kBoxes == kBoxes - 1) {
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) release(&sm.tempty[0][buf]);
@@ -586,7 +471,7 @@ router_products_kernel(const __grid_constant__ CUtensorMap tm_dl, const __grid_c
                             uint32_t o[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const float2 y = __ffma2_rn(make_float2(v[p * 8 + 2 * k], v[p * 8 + 2 * k + 1]), make_float2(sc, sc),
+                                const float2 y = __fadd2_rn(make_float2(v[p * 8 + 2 * k], v[p * 8 + 2 * k + 1]),
                                                             make_float2(__uint_as_float(b[p][k] << 16), __uint_as_float(b[p][k] & 0xffff0000u)));
                                 const __nv_bfloat162 r = __floats2bfloat162_rn(y.x, y.y);
                                 o[k] = *reinterpret_cast<const uint32_t*>(&r);
@@ -875,10 +760,7 @@ RbPlan plan_of(int T, int H, int E) {
 }
 
 struct RbWs {
-    uint16_t* wh;        // W_g: fp16 [E][H] (pairs), else two bf16 parts [2][E][H]
-    float* wscale;       // pairs
-    uint16_t* dlh;       // pairs: dl in fp16 [T][ld]
-    float* tscale;       // pairs
+    uint16_t* w2;        // W_g in two bf16 parts [2][E][H]
     uint16_t* parts;     // dl in bf16 parts: [3][T][ld] (pairs), else [T][3][pitch]
     float* dbpart;
     float* part;
@@ -896,10 +778,7 @@ RbWs carve_router(int T, int H, int E, void* base) {
         off += (bytes + 255) / 256 * 256;
         return r;
     };
-    w.wh = reinterpret_cast<uint16_t*>(take((pl.pair ? 2ull : 4ull) * E * H));
-    w.wscale = reinterpret_cast<float*>(take(pl.pair ? 4ull * E : 0));
-    w.dlh = reinterpret_cast<uint16_t*>(take(pl.pair ? 2ull * T * ld : 0));
-    w.tscale = reinterpret_cast<float*>(take(pl.pair ? 4ull * T : 0));
+    w.w2 = reinterpret_cast<uint16_t*>(take(4ull * E * H));
     w.parts = reinterpret_cast<uint16_t*>(take(6ull * T * (pl.pair ? ld : pl.cols)));
     w.dbpart = reinterpret_cast<float*>(take(4ull * ((T + kPrepTokens - 1) / kPrepTokens) * E));
     w.part = reinterpret_cast<float*>(take(4ull * (static_cast<size_t>(pl.htiles) * pl.etiles + pl.most_groups) * pl.rows * pl.cols));
@@ -907,8 +786,8 @@ RbWs carve_router(int T, int H, int E, void* base) {
     return w;
 }
 
-// [depth][rows][cols] of 16-bit values, rows ld apart, boxes of 64 columns x by rows, 128-byte swizzle.
-bool make_map16(CUtensorMap* m, const void* base, bool bf16, int64_t cols, int64_t rows, int depth, int64_t ld, int by,
+// [depth][rows][cols] of bf16 values, rows ld apart, boxes of 64 columns x by rows, 128-byte swizzle.
+bool make_map16(CUtensorMap* m, const void* base, int64_t cols, int64_t rows, int depth, int64_t ld, int by,
                 int dims_n) {
     EncodeTiledFn fn = tensor_map_encoder();
     if (!fn) return false;
@@ -916,7 +795,7 @@ bool make_map16(CUtensorMap* m, const void* base, bool bf16, int64_t cols, int64
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * ld), static_cast<cuuint64_t>(2 * ld * rows)};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(by), 1};
     const cuuint32_t es[3] = {1, 1, 1};
-    return fn(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, dims_n, const_cast<void*>(base),
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims_n, const_cast<void*>(base),
               dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -938,10 +817,10 @@ cudaError_t launch_direct(const uint16_t* x, const float* Wg, const float* dl, i
                             dx, dWg, db);
 }
 
-template <bool PAIR, int KB, int AS, int NB>
+template <bool PAIR, int KB, int WB, int AS, int NB>
 cudaError_t launch_products(const CUtensorMap (&m)[6], const RouterArgs& g, int groups, cudaStream_t s) {
-    auto kern = router_products_kernel<PAIR, KB, AS, NB>;
-    const size_t smem = sizeof(SmemP<PAIR, KB, AS, NB>) + 1024;
+    auto kern = router_products_kernel<PAIR, KB, WB, AS, NB>;
+    const size_t smem = sizeof(SmemP<KB, WB, AS, NB>) + 1024;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (err != cudaSuccess) return err;
     // a setmaxnreg.inc can only draw on what the block was launched with: refuse a build with less
@@ -1010,35 +889,32 @@ moe_status_t moe_router_backward(int T, int H, int E, const void* x, const float
                    : MOE_ERR_CUDA;
     TileGroups tg = {};
     if (T > 0) {
-        const bool vec = E % 4 == 0;
         CUtensorMap m[6];
-        bool mapped = make_map16(&m[2], dx0 ? dx0 : dx, true, H, T, 1, H, 32, 2) && make_map16(&m[3], dx, true, H, T, 1, H, 32, 2);
-        if (p.pair) {
-            auto prep = E <= 256 ? (vec ? router_prep_dl_kernel<2, true> : router_prep_dl_kernel<2, false>)
-                                 : (vec ? router_prep_dl_kernel<4, true> : router_prep_dl_kernel<4, false>);
-            if (!ok(launch_dependent(router_prep_w_kernel, dim3(E), dim3(256), 0, s, Wg, H, w.wh, w.wscale)) ||
-                !ok(launch_dependent(prep, dim3(db_blocks), dim3(256), 0, s, dlogits, w.wscale, T, E, ld, w.dlh, w.tscale, w.parts, w.dbpart)))
-                return MOE_ERR_CUDA;
-            mapped = mapped && make_map16(&m[0], w.dlh, false, E, T, 1, ld, 128, 2) &&
-                     make_map16(&m[1], w.wh, false, H, E, 1, H, 64, 3) && make_map16(&m[4], x, true, H, T, 1, H, 64, 3) &&
-                     make_map16(&m[5], w.parts, true, E, T, 3, ld, 64, 3);
-        } else {
-            const int w_blocks = static_cast<int>((static_cast<int64_t>(E) * H + kPrepW - 1) / kPrepW), ts = p.cols <= 64 ? 128 : 64;
-            if (!ok(launch_dependent(vec ? router_prep_parts_kernel<true> : router_prep_parts_kernel<false>, dim3(db_blocks + w_blocks),
-                                     dim3(256), 0, s, dlogits, Wg, T, H, E, p.cols, db_blocks, w.parts, w.dbpart, w.wh)))
-                return MOE_ERR_CUDA;
-            mapped = mapped && make_map16(&m[0], w.parts, true, 3 * p.cols, T, 1, 3 * p.cols, 128, 2) &&
-                     make_map16(&m[1], w.wh, true, H, E, 2, H, 64, 3) && make_map16(&m[4], x, true, H, T, 1, H, ts, 3) &&
-                     make_map16(&m[5], w.parts, true, 3 * p.cols, T, 1, 3 * p.cols, ts, 3);
-        }
+        // dl's parts: three planes of T rows (pairs), or side by side in each row
+        const int width = p.pair ? ld : p.cols, ts = p.cols <= 64 ? 128 : 64;
+        const int64_t row = p.pair ? ld : 3 * p.cols, part = p.pair ? static_cast<int64_t>(T) * ld : p.cols;
+        const int w_blocks = static_cast<int>((static_cast<int64_t>(E) * H + kPrepW - 1) / kPrepW);
+        const bool vec = E % 4 == 0;
+        auto prep = E <= 128   ? (vec ? router_prep_parts_kernel<1, true> : router_prep_parts_kernel<1, false>)
+                    : E <= 256 ? (vec ? router_prep_parts_kernel<2, true> : router_prep_parts_kernel<2, false>)
+                               : (vec ? router_prep_parts_kernel<4, true> : router_prep_parts_kernel<4, false>);
+        if (!ok(launch_dependent(prep, dim3(db_blocks + w_blocks), dim3(256), 0, s, dlogits, Wg, T, H, E, width, row, part, db_blocks,
+                                 w.parts, w.dbpart, w.w2)))
+            return MOE_ERR_CUDA;
+        bool mapped = make_map16(&m[1], w.w2, H, E, 2, H, 64, 3) && make_map16(&m[2], dx0 ? dx0 : dx, H, T, 1, H, 32, 2) &&
+                      make_map16(&m[3], dx, H, T, 1, H, 32, 2) && make_map16(&m[4], x, H, T, 1, H, ts, 3);
+        if (p.pair)
+            mapped = mapped && make_map16(&m[0], w.parts, E, T, 3, ld, 128, 3) && make_map16(&m[5], w.parts, E, T, 3, ld, 64, 3);
+        else
+            mapped = mapped && make_map16(&m[0], w.parts, row, T, 1, row, 128, 2) && make_map16(&m[5], w.parts, row, T, 1, row, ts, 3);
         if (!mapped) return MOE_ERR_CUDA;
         RouterArgs g;
         g.T = T;
         g.H = H;
         g.E = E;
         g.has_base = dx0 != nullptr;
-        const int tok = p.pair ? 256 : 128, groups = std::min(p.pair ? num_sms / 2 : num_sms, p.most_groups);
-        g.Ux = (H + 255) / 256 * ((T + tok - 1) / tok);
+        const int tok = p.pair ? 256 : 128, panel = E > 256 ? 128 : 256, groups = std::min(p.pair ? num_sms / 2 : num_sms, p.most_groups);
+        g.Ux = (H + panel - 1) / panel * ((T + tok - 1) / tok);
         g.Uw = p.U;
         g.Gx = std::min(groups, g.Ux);
         g.Gw = std::min(groups, g.Uw);
@@ -1048,14 +924,13 @@ moe_status_t moe_router_backward(int T, int H, int E, const void* x, const float
         }
         g.etiles = p.etiles;
         g.pitch = p.cols;
-        g.tscale = w.tscale;
         g.part = w.part;
         g.status = status;
         const int used = std::max(g.Gx, g.Gw);
-        const cudaError_t err = E <= 64    ? launch_products<false, 2, 4, 3>(m, g, used, s)
-                                : E <= 128 ? launch_products<false, 4, 2, 2>(m, g, used, s)
-                                : E <= 256 ? launch_products<true, 4, 4, 3>(m, g, used, s)
-                                           : launch_products<true, 8, 2, 2>(m, g, used, s);
+        const cudaError_t err = E <= 64    ? launch_products<false, 2, 4, 4, 3>(m, g, used, s)
+                                : E <= 128 ? launch_products<false, 4, 4, 2, 2>(m, g, used, s)
+                                : E <= 256 ? launch_products<true, 8, 2, 2, 2>(m, g, used, s)
+                                           : launch_products<true, 16, 1, 2, 2>(m, g, used, s);
         if (!ok(err)) return MOE_ERR_CUDA;
     }
     return ok(launch_dependent(router_finish_kernel, dim3((H + 1023) / 1024, E), dim3(256), 0, s, w.part, w.dbpart, tg, H, E, p.rows,

@@ -407,16 +407,13 @@ moe_status_t moe_balance_loss_backward(int T, int E, int k, const float* logits,
  *       aligned
  * The products run on the tensor cores: dWg with dlogits in three bf16 parts
  * (its 24 bits) against x, sums promoted to fp32 registers every 128 tokens;
- * dx up to 128 experts with W_g and dlogits in bf16 pairs (16 bits), above in
- * fp16 (11 bits, an eighth of dx's own rounding step), each expert and then each
- * token scaled by a power of two: there values below 2^-23 of the largest W_g of
- * their expert, or of the largest term of their token, lose bits, below 2^-34 all
- * of them. Up to 512 tokens and 2^25 products T H E both run in fp32 on the CUDA
- * cores. Results repeat bit for bit.
+ * dx with W_g and dlogits in two bf16 parts each (16 bits: a term is off by at
+ * most 3 2^-18 of it, whatever its size within fp32's normal range), fp32 sums.
+ * Up to 512 tokens and 2^25 products T H E both run in fp32 on the CUDA cores.
+ * Results repeat bit for bit.
  * A dlogits row of zeros leaves its dx row at dx0. Values beyond 3e38 count as
- * not finite; those spread only as the formulas spread them, except that above
- * 128 experts one whose W_g row holds such a value makes every dx row NaN or
- * infinite. T = 0 gives the bases, or zeros.
+ * not finite; those spread only as the formulas spread them. T = 0 gives the
+ * bases, or zeros.
  * H as everywhere (a multiple of 128, at most 16384), E up to MOE_MAX_EXPERTS,
  * T below 2^24.
  */
