@@ -148,8 +148,8 @@ __device__ __forceinline__ float group_sum(float v) {
 __device__ __forceinline__ float exp_from(float v, float c) { return exp2f(fmaf(v, kLog2e, -c)); }
 
 // Rows whose maximum or lse is farther than this from zero (all of a row at the type's lowest value, say) are shifted to
-// it first: the rounding of c shows in lse, as much as lse's own, and from about 2^30 on would leave exp2's range; the
-// gradient, which has no sum to undo them, would show that of c and of lse.
+// it first: the rounding of c shows in the forward's lse, as much as lse's own, and from about 2^30 on would leave exp2's
+// range.
 constexpr float kFar = 64.0f;
 
 __device__ __forceinline__ double warp_sum(double v) {
@@ -487,28 +487,27 @@ balance_backward_kernel(const float* __restrict__ logits, const float* __restric
 #pragma unroll
                 for (int i = 1; i < V; ++i) m = fmaxf(m, v[i]);
                 m = group_max<G>(m);
-                float sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < V; ++i) sum += exp2f((v[i] - m) * kLog2e);
-                sum = group_sum<G>(sum);
                 if (far) {
-                    lc = log2f(sum);
+                    lc = 0.0f;
 #pragma unroll
                     for (int i = 0; i < V; ++i) v[i] -= m;
                 }
             }
-            float dot = 0.0f;
+            // exp(l - lse) up to a factor near 1 that the rounding of lse and of lse log2 e leaves: the row's sum undoes it
+            float dot = 0.0f, sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 v[i] = exp_from(v[i], lc);
+                sum += v[i];
                 dot = fmaf(v[i], c[i], dot);
             }
+            sum = group_sum<G>(sum);
             dot = group_sum<G>(dot);
             if (t < b) {
-                const float shift = fmaf(zc, l, -dot);
+                const float r = 1.0f / sum, shift = fmaf(zc, l, -dot * r);
                 float* out = dlogits + static_cast<int64_t>(t) * E;
 #pragma unroll
-                for (int i = 0; i < V; ++i) v[i] = on ? v[i] * (c[i] + shift) : 0.0f;
+                for (int i = 0; i < V; ++i) v[i] = on ? v[i] * r * (c[i] + shift) : 0.0f;
                 if constexpr (VEC) {
 #pragma unroll
                     for (int q = 0; q < V / 4; ++q)

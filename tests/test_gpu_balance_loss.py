@@ -272,3 +272,25 @@ def test_captured_behind_a_memset_a_copy_and_a_joined_stream(T):
         g.replay()
         for x, y in zip(want, c.results()):
             assert np.array_equal(x, y)
+
+
+@pytest.mark.parametrize("T,E", [(200, 8), (2000, 8), (2000, 60), (2000, 256), (1500, 511)])
+def test_probabilities_of_the_gradient_do_not_lose_bits_where_lse_is_large(T, E):
+    # Rows up to 63 from zero whose logits lie within 1 of each other. The exponent of a probability is a = (l - lse) log2 e,
+    # |a| <= log2 E + 1.45: rounded once, half a step is 2^floor(log2 a) u, a relative error of the exponential ln 2 times
+    # that; exp2 is off by 2 steps, 4 u, and the constant log2 e by less than u over a row. All of it counts once for the
+    # value and once in the row's sum, which has at most 16 + 5 additions; then a quotient and a product. Rounding
+    # lse log2 e, or lse, scales a row alike, which dividing by its sum undoes: nothing grows with lse. With beta alone the
+    # gradient is p times three more factors; with alpha alone a sum over the experts more.
+    r = np.random.default_rng(E + T)
+    shift = r.uniform(40, 62.5, (T, 1)) * r.choice([-1, 1], (T, 1))
+    logits = (shift + r.uniform(-0.5, 0.5, (T, E))).astype(np.float32)
+    adds = min(E, 16) + 5
+    one = 4 + 1 + np.log(2) * 2.0 ** np.floor(np.log2(np.log2(E) + 1.45))
+    p_u = 2 * one + adds + 2
+    for alpha, beta, tol in ((0.0, 1.0, p_u + 6), (1.0, 0.0, 2 * p_u + adds + 6)):
+        c = Case(T, E, min(E, 8), logits=logits, alpha=alpha, beta=beta).forward().backward()
+        dl = c.results()[5]
+        want = ref.balance(logits, c.idx, None, [0, T], alpha, beta, c.k)
+        g, mag = ref.balance_grad(want, [0, T], alpha, beta, c.k)
+        assert (np.abs(dl - g) <= tol * U * mag).all(), (np.abs(dl - g) / mag).max() / U
