@@ -371,7 +371,7 @@ balance_reduce_kernel(const int32_t* __restrict__ offsets, int T, int E, int k, 
                       BalWs w, float* __restrict__ loss, int32_t* __restrict__ counts, float* __restrict__ mean_prob,
                       int32_t* valid, int* status) {
     constexpr int kRows = kRedThreads / COLS, kW = kRedThreads / 32;
-    __shared__ float sm_p[kW][COLS];
+    __shared__ double sm_p[kW][COLS];
     __shared__ int sm_h[kW][COLS];
     __shared__ double sm_z[kW];
     __shared__ int sm_n[kW];
@@ -384,9 +384,8 @@ balance_reduce_kernel(const int32_t* __restrict__ offsets, int T, int E, int k, 
     const int a = seq_start(offsets, s, T), b = seq_start(offsets, s + 1, T);
     if (threadIdx.x == 0 && blockIdx.x == 0) check_offsets(offsets, s, a, b, status);
     const int lo = a / C, hi = b > a ? (b - 1) / C + 1 : lo;       // chunks that hold some of the sequence
-    float p = 0.0f;
+    double p = 0.0, z = 0.0;       // a run's sums are fp32, their total has more bits
     int h = 0, n = 0;
-    double z = 0.0;
     for (int c = lo + threadIdx.x; c < hi; c += kRedThreads) {
         n += w.nval[c + s];
         if (blockIdx.x == 0) z += w.zsum[c + s];

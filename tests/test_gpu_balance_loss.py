@@ -294,3 +294,28 @@ def test_probabilities_of_the_gradient_do_not_lose_bits_where_lse_is_large(T, E)
         want = ref.balance(logits, c.idx, None, [0, T], alpha, beta, c.k)
         g, mag = ref.balance_grad(want, [0, T], alpha, beta, c.k)
         assert (np.abs(dl - g) <= tol * U * mag).all(), (np.abs(dl - g) / mag).max() / U
+
+
+def test_runs_of_tokens_are_joined_in_64_bits():
+    # Every sum within a run of tokens is exact here: a row is 1 on expert 0, or 2^-9 on each of 512 experts, and a run's
+    # sums are below 2^12 in multiples of 2^-9. Their totals have more bits than fp32. Joined in 64 bits they are exact, and
+    # mean_prob is the total over the valid tokens rounded once; joined in fp32, a warp's share near 2^17 moves in steps
+    # of 2^-6 and every few masks end on another value.
+    ensure_lib()
+    T, E = 1 << 20, 512
+    r = torch.Generator(device="cuda").manual_seed(3)
+    even = torch.rand(T, generator=r, device="cuda") < 0.003
+    logits = torch.full((T, E), -300.0, device="cuda")
+    logits[:, 0] = 0.0
+    logits[even] = 0.0
+    new = lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device="cuda")
+    loss, counts, mp, lse, valid = new(2), new(1, E, dt=torch.int32), new(1, E), new(T), new(3, dt=torch.int32)
+    ws = new(api.moe_balance_workspace_size(T, E), dt=torch.uint8)
+    idx = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    for seed in range(64):
+        mask = (torch.rand(T, generator=r, device="cuda") < 0.97).to(torch.uint8)
+        api.moe_balance_loss(T, E, 1, logits, idx, mask, None, 1, 1.0, 0.0, loss, counts, mp, lse, valid, ws)
+        n, m = int(mask.sum()), int((mask.bool() & even).sum())
+        want = np.full(E, m / 512.0) / n
+        want[0] = (n - m + m / 512.0) / n
+        assert np.array_equal(to_np(mp)[0], want.astype(np.float32)), seed
