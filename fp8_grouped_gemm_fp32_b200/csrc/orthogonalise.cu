@@ -1027,9 +1027,12 @@ ortho_narrow_kernel(const __grid_constant__ CUtensorMap tm_y, const __grid_const
 // ---------------------------------------------------------------- workspace and launches
 // A wave holds enough matrices to give every CTA pair a tile of the symmetric products, twice over, and never
 // fewer than two (one fills the other's waits); a batch is cut into equal waves that use the workspace in turn.
-int wave_of(int mats, int M, int N, int interleaved) {
+int most_of(int M, int N) {
     const int nb = (std::min(M, N) + 255) / 256, ns = nb * (nb + 1) / 2;
-    const int most = std::max(2, (148 + ns - 1) / ns);
+    return std::max(2, (148 + ns - 1) / ns);
+}
+int wave_of(int mats, int M, int N, int interleaved) {
+    const int most = most_of(M, N);
     const int waves = (mats + most - 1) / most;
     int w = (mats + waves - 1) / waves;
     if (interleaved) w = (w + 1) / 2 * 2;            // a wave starts at a first matrix
@@ -1172,6 +1175,26 @@ NarrowWs carve_narrow(int mats, int M, int N, void* base) {
     return w;
 }
 
+// What `mats` matrices need, and what they or any fewer do: equal waves of a large batch may be smaller than a smaller
+// batch's one wave, and a short side's kernel goes by the batch.
+size_t need_of(int mats, int M, int N, int interleaved) {
+    if (use_narrow(mats, M, N)) return carve_narrow(mats, M, N, nullptr).total;
+    return carve_ortho(wave_of(mats, M, N, interleaved), M, N, nullptr).total;
+}
+size_t most_needed(int mats, int M, int N, int interleaved) {
+    size_t most = 0;
+    if (use_narrow(1, M, N)) {
+        const int t = narrow_tiles(M, N);
+        most = carve_narrow(t <= 4 ? mats : std::min(mats, kNarrowSms / t), M, N, nullptr).total;
+    }
+    if (!use_narrow(mats, M, N)) {
+        int wave = std::min(mats, most_of(M, N));
+        if (interleaved) wave = (wave + 1) / 2 * 2;
+        most = std::max(most, carve_ortho(wave, M, N, nullptr).total);
+    }
+    return most;
+}
+
 template <bool F32>
 cudaError_t launch_prepare(const void* G, int mats, const OrthoArgs& g, const OrthoWs& w, double eps, double xscale,
                            cudaStream_t s) {
@@ -1270,9 +1293,7 @@ extern "C" {
 
 size_t moe_orthogonalise_workspace_size(int batch, int M, int N, int interleaved) {
     if (check_ortho(batch, M, N, interleaved) != MOE_OK || batch == 0) return 0;
-    const int mats = batch * (interleaved ? 2 : 1);
-    if (use_narrow(mats, M, N)) return carve_narrow(mats, M, N, nullptr).total;
-    return carve_ortho(wave_of(mats, M, N, interleaved), M, N, nullptr).total;
+    return most_needed(batch * (interleaved ? 2 : 1), M, N, interleaved);
 }
 
 moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const void* G, int g_type, int steps, float a,
@@ -1289,7 +1310,7 @@ moe_status_t moe_orthogonalise(int batch, int M, int N, int interleaved, const v
     const bool narrow = use_narrow(mats, M, N);
     const OrthoWs w = carve_ortho(wave, M, N, ws);
     const NarrowWs nw = carve_narrow(mats, M, N, ws);
-    if (ws_bytes < (narrow ? nw.total : w.total)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < need_of(mats, M, N, interleaved)) return MOE_ERR_WORKSPACE_TOO_SMALL;
     int num_sms, *status;
     if ((st = current_device(&num_sms, &status)) != MOE_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -439,7 +439,8 @@ moe_status_t moe_router_backward(int T, int H, int E, const void* x, const float
  *   steps       1 .. 32
  *   ws          scratch of moe_orthogonalise_workspace_size(batch, M, N,
  *               interleaved) bytes, 256-byte aligned; a large batch is run in
- *               waves that use it in turn
+ *               waves that use it in turn. The size for a batch serves any
+ *               smaller one too
  * Products are fp16 with fp32 sums; X is carried in 22 bits, so that the
  * result differs from exact arithmetic by about bf16's own rounding also where
  * G is of low rank. Large matrices (both sides from 1024, one at least 1.5 times

@@ -230,3 +230,14 @@ def test_several_tiles_a_cta_of_several_matrices_repeat_and_equal_each_alone(bat
         assert torch.equal(want, alone)
     for _ in range(20):
         assert torch.equal(done(run(G, batch, M, N, ws=ws)), want)
+
+
+@pytest.mark.parametrize("large,small,M,N,inter", [(26, 25, 520, 520, False), (19, 18, 100, 1000, False), (13, 12, 256, 512, True)])
+def test_a_smaller_batch_in_a_larger_ones_workspace(large, small, M, N, inter):
+    G = torch.randn(large, 2 * M if inter else M, N, generator=torch.Generator("cuda").manual_seed(M), device="cuda")
+    ws = torch.empty(api.moe_orthogonalise_workspace_size(large, M, N, inter), dtype=torch.uint8, device="cuda")
+    for n in (large, small, large):
+        O = done(run(G[:n].contiguous(), n, M, N, inter, ws=ws))
+        for i in (0, n - 1):
+            o, x = (ref.split(O[i])[1], ref.split(G[i])[1]) if inter else (O[i], G[i])
+            assert ref.rel_norm(o, ref.orthogonalise(x)) <= 2.0 ** -8 + 2.0 ** -7

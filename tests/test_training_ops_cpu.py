@@ -199,3 +199,25 @@ def test_binding_refuses_host_and_strided_tensors(L):
         api.moe_balance_loss(8, 8, 1, t, t, None, None, 1, 0.1, 0.0, t, t, t, t, t, t)
     with pytest.raises(ValueError):
         api.moe_router_backward(8, 128, 8, t, t, t, None, None, None, t, t, t, t)
+
+
+@pytest.mark.parametrize("M,N,inter", [(520, 520, False), (100, 1000, False), (128, 5000, True), (1000, 100, False), (60, 70, False),
+                                       (256, 512, True), (300, 129, False), (2048, 4096, False), (16384, 100, False),
+                                       (128, 16384, True)])
+def test_orthogonalise_workspace_of_a_batch_serves_every_smaller_one(L, M, N, inter):
+    sizes = [api.moe_orthogonalise_workspace_size(b, M, N, inter) for b in range(1, 400)]
+    assert sizes == sorted(sizes)
+
+
+def test_orthogonalise_takes_the_workspace_of_a_larger_batch(L):
+    # Refused before any device work where the workspace is too small: a batch that fits goes on, and this machine has no
+    # device to go on to.
+    call = lambda batch, M, N, nbytes: L.moe_orthogonalise(batch, M, N, 0, p(OKP), 0, 5, *ref.ORTHO, 1e-7, 1.0, p(OKP), p(OKP),
+                                                           nbytes, None)
+    if torch.cuda.is_available():
+        pytest.skip("would launch")
+    for M, N in ((520, 520), (100, 1000)):
+        for large in (19, 26, 30):
+            n = api.moe_orthogonalise_workspace_size(large, M, N)
+            assert all(call(b, M, N, n) not in (SMALL, api.MOE_OK) for b in range(1, large + 1))
+    assert call(2, 520, 520, 4096) == SMALL
