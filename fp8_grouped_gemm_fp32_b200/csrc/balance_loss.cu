@@ -60,9 +60,11 @@ struct BalWs {
     size_t total;
 };
 
+// Sized so that a larger T, E or S never takes less: chunks as if none were longer than 16 tokens until there are
+// kMaxChunks, column blocks of 8.
 BalWs carve_balance(int T, int E, int S, void* base) {
     BalWs w;
-    const size_t cuts = static_cast<size_t>(chunks_of(T)) + S, nx = (E + red_cols(S) - 1) / red_cols(S);
+    const size_t cuts = static_cast<size_t>(std::min(kMaxChunks, (T + 15) / 16)) + S, nx = (E + 7) / 8;
     uint8_t* p = static_cast<uint8_t*>(base);
     size_t off = 0;
     auto take = [&](size_t bytes) {

@@ -362,7 +362,8 @@ size_t moe_train_logits_offset(const moe_config_t* cfg);
  *   counts      [S, E] int32 out, mean_prob [S, E] fp32 out
  *   lse         [T] fp32 out: 0 for masked tokens
  *   seq_valid   [S + 2] int32 out: n_0 .. n_{S-1}, S', N
- *   ws          scratch of moe_balance_workspace_size(T, E, S) bytes
+ *   ws          scratch of moe_balance_workspace_size(T, E, S) bytes; that of
+ *               larger arguments will do
  * Sums are fp32 within 296 runs of tokens and fp64 across them (of lse^2: fp64),
  * in a fixed order: results repeat bit for bit. Outputs overlap nothing. A logit of -inf has p = 0; a valid row
  * with no finite logit, a NaN or +inf makes its sequence's losses NaN, as the

@@ -221,3 +221,20 @@ def test_orthogonalise_takes_the_workspace_of_a_larger_batch(L):
             n = api.moe_orthogonalise_workspace_size(large, M, N)
             assert all(call(b, M, N, n) not in (SMALL, api.MOE_OK) for b in range(1, large + 1))
     assert call(2, 520, 520, 4096) == SMALL
+
+
+@pytest.mark.parametrize("E", [8, 60, 256, 512])
+def test_balance_workspace_of_a_size_serves_every_smaller_one(L, E):
+    size = api.moe_balance_workspace_size
+    for S in (1, 16, 17, 100):
+        got = [size(T, E, S) for T in range(0, 12000, 7)]
+        assert got == sorted(got)
+    for T in (64, 4736, 4737, 9000):
+        got = [size(T, E, S) for S in range(1, 200)]
+        assert got == sorted(got)
+
+
+@pytest.mark.parametrize("H,E", [(128, 8), (1408, 100), (2048, 160), (512, 512)])
+def test_router_workspace_of_a_count_of_tokens_serves_every_smaller_one(L, H, E):
+    got = [api.moe_router_backward_workspace_size(T, H, E) for T in range(0, 3000)]
+    assert got == sorted(got)
