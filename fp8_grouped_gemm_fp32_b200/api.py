@@ -277,25 +277,42 @@ def moe_backward(cfg, x, Wg, W13, S13, W13T, S13T, W2T, S2T, topk_idx, topk_w, s
 
 
 # ---------------------------------------------------------------- balance loss, the router's gradient, updates
-def _args(*tensors):
-    """The tensors' pointers (None: null), all checked to be contiguous and on the current device, where the library
-    launches whatever device a pointer is of."""
+_F32, _I32, _BF16 = torch.float32, torch.int32, torch.bfloat16
+
+
+def _args(call, *specs):
+    """The pointers of (name, tensor, type, least number of elements) each (tensor None: null; type None: any), all
+    checked to be of that type, large enough, contiguous and on the current device, where the library launches
+    whatever device a pointer is of."""
     out, dev = [], None
-    for t in tensors:
+    for name, t, dtype, n in specs:
         if t is None:
             out.append(None)
             continue
-        d = t.get_device()
-        if d != dev:
-            if d < 0:
-                raise ValueError("moe_fp8 entry points take CUDA tensors")
-            dev = torch._C._cuda_getDevice()
-            if d != dev:
-                raise ValueError(f"a tensor of cuda:{d} in a call on the current device cuda:{dev}")
+        if dtype is not None and t.dtype is not dtype:
+            raise ValueError(f"{call}: {name} is {t.dtype}, not {dtype}")
+        if t.numel() < n:
+            raise ValueError(f"{call}: {name} has {t.numel()} elements, not {n}")
         if not t.is_contiguous():
             raise ValueError("moe_fp8 entry points take contiguous tensors")
+        d = t.get_device()
+        if d != dev:
+            if dev is not None:
+                raise ValueError(f"{call}: {name} is on {t.device}, the tensors before it are not")
+            dev = d
         out.append(t.data_ptr())
+    if dev is not None:
+        if dev < 0:
+            raise ValueError("moe_fp8 entry points take CUDA tensors")
+        current = torch._C._cuda_getDevice()
+        if dev != current:
+            raise ValueError(f"{call}: tensors of cuda:{dev} in a call on the current device cuda:{current}")
     return out
+
+
+def _mask(t, T):
+    """The spec of a token mask: u8, or bool, whose values are 0 and 1 too."""
+    return "token_mask", t, torch.bool if t is not None and t.dtype is torch.bool else torch.uint8, T
 
 
 def moe_train_logits(cfg: Config, ws: torch.Tensor) -> torch.Tensor:
@@ -313,7 +330,10 @@ def moe_balance_workspace_size(T: int, E: int, S: int = 1) -> int:
 def moe_balance_loss(T, E, k, logits, topk_idx, token_mask, seq_offsets, S, alpha, beta, loss, counts, mean_prob, lse,
                      seq_valid, ws, stream=None):
     """Balance loss and z-loss of the router's logits; token_mask, seq_offsets nullable."""
-    p = _args(logits, topk_idx, token_mask, seq_offsets, loss, counts, mean_prob, lse, seq_valid, ws)
+    p = _args("moe_balance_loss", ("logits", logits, _F32, T * E), ("topk_idx", topk_idx, _I32, T * k), _mask(token_mask, T),
+              ("seq_offsets", seq_offsets, _I32, S + 1), ("loss", loss, _F32, 2), ("counts", counts, _I32, S * E),
+              ("mean_prob", mean_prob, _F32, S * E), ("lse", lse, _F32, T), ("seq_valid", seq_valid, _I32, S + 2),
+              ("ws", ws, None, 0))
     _check(lib().moe_balance_loss(T, E, k, *p[:4], S, alpha, beta, *p[4:], _nbytes(ws), _stream(stream)),
            "moe_balance_loss")
 
@@ -321,7 +341,9 @@ def moe_balance_loss(T, E, k, logits, topk_idx, token_mask, seq_offsets, S, alph
 def moe_balance_loss_backward(T, E, k, logits, lse, counts, seq_valid, token_mask, seq_offsets, S, alpha, beta, dloss,
                               dlogits, stream=None):
     """dlogits [T, E] of moe_balance_loss; dloss [2] nullable (ones)."""
-    p = _args(logits, lse, counts, seq_valid, token_mask, seq_offsets, dloss, dlogits)
+    p = _args("moe_balance_loss_backward", ("logits", logits, _F32, T * E), ("lse", lse, _F32, T),
+              ("counts", counts, _I32, S * E), ("seq_valid", seq_valid, _I32, S + 2), _mask(token_mask, T),
+              ("seq_offsets", seq_offsets, _I32, S + 1), ("dloss", dloss, _F32, 2), ("dlogits", dlogits, _F32, T * E))
     _check(lib().moe_balance_loss_backward(T, E, k, *p[:6], S, alpha, beta, *p[6:], _stream(stream)),
            "moe_balance_loss_backward")
 
@@ -332,7 +354,9 @@ def moe_router_backward_workspace_size(T: int, H: int, E: int) -> int:
 
 def moe_router_backward(T, H, E, x, Wg, dlogits, dx0, dWg0, db0, dx, dWg, db, ws, stream=None):
     """dx = dx0 + dlogits Wg, dWg = dWg0 + dlogits^T x, db = db0 + sum of dlogits; the bases nullable."""
-    p = _args(x, Wg, dlogits, dx0, dWg0, db0, dx, dWg, db, ws)
+    p = _args("moe_router_backward", ("x", x, _BF16, T * H), ("Wg", Wg, _F32, E * H), ("dlogits", dlogits, _F32, T * E),
+              ("dx0", dx0, _BF16, T * H), ("dWg0", dWg0, _F32, E * H), ("db0", db0, _F32, E), ("dx", dx, _BF16, T * H),
+              ("dWg", dWg, _F32, E * H), ("db", db, _F32, E), ("ws", ws, None, 0))
     _check(lib().moe_router_backward(T, H, E, *p, _nbytes(ws), _stream(stream)), "moe_router_backward")
 
 
@@ -342,9 +366,8 @@ def moe_orthogonalise_workspace_size(batch: int, M: int, N: int, interleaved: bo
 
 def moe_orthogonalise(batch, M, N, interleaved, G, steps, a, b, c, eps, scale, O, ws, stream=None):
     """O = scale * the quintic Newton-Schulz iterate of each matrix of G (bf16 or fp32) after `steps` steps."""
-    if G.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError("moe_orthogonalise takes bf16 or fp32 matrices")
-    g, o, w = _args(G, O, ws)
-    _check(lib().moe_orthogonalise(batch, M, N, int(bool(interleaved)), g,
-                                   TYPE_FP32 if G.dtype == torch.float32 else TYPE_BF16, steps, a, b, c, eps, scale, o, w,
-                                   _nbytes(ws), _stream(stream)), "moe_orthogonalise")
+    f32 = G.dtype is _F32
+    n = batch * M * N * (2 if interleaved else 1)
+    g, o, w = _args("moe_orthogonalise", ("G", G, _F32 if f32 else _BF16, n), ("O", O, _BF16, n), ("ws", ws, None, 0))
+    _check(lib().moe_orthogonalise(batch, M, N, int(bool(interleaved)), g, TYPE_FP32 if f32 else TYPE_BF16, steps, a,
+                                   b, c, eps, scale, o, w, _nbytes(ws), _stream(stream)), "moe_orthogonalise")

@@ -238,3 +238,43 @@ def test_balance_workspace_of_a_size_serves_every_smaller_one(L, E):
 def test_router_workspace_of_a_count_of_tokens_serves_every_smaller_one(L, H, E):
     got = [api.moe_router_backward_workspace_size(T, H, E) for T in range(0, 3000)]
     assert got == sorted(got)
+
+
+def _binding_calls():
+    """Calls of the bindings with host tensors of the right types and sizes, by operator: name -> (call, tensors)."""
+    T, E, k, S, H = 12, 8, 2, 3, 128
+    f = lambda *s: torch.zeros(*s)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    h = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    b = lambda *s: torch.zeros(*s, dtype=torch.uint8)
+    fwd = dict(logits=f(T, E), topk_idx=i(T, k), token_mask=b(T), seq_offsets=i(S + 1), loss=f(2), counts=i(S, E),
+               mean_prob=f(S, E), lse=f(T), seq_valid=i(S + 2), ws=b(1 << 20))
+    bwd = dict(logits=f(T, E), lse=f(T), counts=i(S, E), seq_valid=i(S + 2), token_mask=b(T), seq_offsets=i(S + 1),
+               dloss=f(2), dlogits=f(T, E))
+    rb = dict(x=h(T, H), Wg=f(E, H), dlogits=f(T, E), dx0=h(T, H), dWg0=f(E, H), db0=f(E), dx=h(T, H), dWg=f(E, H), db=f(E),
+              ws=b(1 << 20))
+    ortho = dict(G=f(2, 2 * H, 16), O=h(2, 2 * H, 16), ws=b(1 << 20))
+    return {
+        "balance": (lambda a: api.moe_balance_loss(T=T, E=E, k=k, S=S, alpha=0.1, beta=0.0, **a), fwd),
+        "balance_backward": (lambda a: api.moe_balance_loss_backward(T=T, E=E, k=k, S=S, alpha=0.1, beta=0.0, **a), bwd),
+        "router": (lambda a: api.moe_router_backward(T=T, H=H, E=E, **a), rb),
+        "ortho": (lambda a: api.moe_orthogonalise(2, H, 16, True, a["G"], 5, *ref.ORTHO, 1e-7, 1.0, a["O"], a["ws"]), ortho)}
+
+
+@pytest.mark.parametrize("op", ["balance", "balance_backward", "router", "ortho"])
+def test_binding_refuses_other_types_and_smaller_tensors(L, op):
+    call, good = _binding_calls()[op]
+    with pytest.raises(ValueError, match="CUDA tensors"):                  # all else is right
+        call(good)
+    for name, t in good.items():
+        if name != "ws":                                                   # (the library is given its size)
+            other = torch.int64 if t.dtype in (torch.int32, torch.uint8) else torch.float16
+            with pytest.raises(ValueError, match=name):
+                call(dict(good, **{name: t.to(other)}))
+            with pytest.raises(ValueError, match=name):
+                call(dict(good, **{name: t.view(-1)[:-1].contiguous()}))
+            with pytest.raises(ValueError, match="CUDA tensors"):          # a larger one will do
+                call(dict(good, **{name: torch.cat([t.view(-1), t.view(-1)])}))
+    if "token_mask" in good:
+        with pytest.raises(ValueError, match="CUDA tensors"):
+            call(dict(good, token_mask=good["token_mask"].bool()))
