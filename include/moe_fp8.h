@@ -442,9 +442,13 @@ moe_status_t moe_router_backward(int T, int H, int E, const void* x, const float
  *               interleaved) bytes, 256-byte aligned; a large batch is run in
  *               waves that use it in turn. The size for a batch serves any
  *               smaller one too
- * Products are fp16 with fp32 sums; X is carried in 22 bits, so that the
- * result differs from exact arithmetic by about bf16's own rounding also where
- * G is of low rank. Large matrices (both sides from 1024, one at least 1.5 times
+ * Products are fp16 with fp32 sums; X is carried in 22 bits, so that at five
+ * steps the result differs from exact arithmetic by about bf16's own rounding
+ * also where G is of low rank. Rounding noise in directions that G lacks grows by
+ * a every step: for G of exactly rank r and a shorter side s it comes to at most
+ * about (2^-21 + s 2^-29) a^steps / sqrt(r) of the result's norm, above bf16's
+ * rounding from 7 to 10 steps on (fp32 arithmetic: a third as much to twice as
+ * much). Large matrices (both sides from 1024, one at least 1.5 times
  * the other) take their first two steps at once, in products of the smaller
  * Gram matrix: the same iterate, other roundings. A matrix of zeros (with eps > 0) gives zeros; a matrix
  * with an infinity or a NaN gives NaN, the others of the batch are unaffected.

@@ -241,3 +241,43 @@ def test_a_smaller_batch_in_a_larger_ones_workspace(large, small, M, N, inter):
         for i in (0, n - 1):
             o, x = (ref.split(O[i])[1], ref.split(G[i])[1]) if inter else (O[i], G[i])
             assert ref.rel_norm(o, ref.orthogonalise(x)) <= 2.0 ** -8 + 2.0 ** -7
+
+
+@pytest.mark.parametrize("M,N", [(64, 64), (900, 100), (128, 700), (300, 200), (512, 1024), (1024, 1600)])
+@pytest.mark.parametrize("steps", [5, 8, 10, 12])
+def test_exactly_low_rank_at_many_steps(M, N, steps):
+    # What the header states: X off by at most 2^-22 of a value, and as much from B's rounding times what the first fp16 value
+    # lacks of X (2^-11 of either); of a step's sums over s, s / 16 additions drop at most 2^-23 of a running sum each, a
+    # quarter of it on average over the drop and the sum's way up, s 2^-29 of a X in all; a to the power of the steps
+    # multiplies them. At rank 1, one step at a time, the same iteration in fp32 is no closer.
+    for r in (1, 8, 32):
+        G = ref.low_rank(M, N, r, device="cuda")
+        O = done(run(G[None].contiguous(), 1, M, N, steps=steps))[0]
+        exact = ref.orthogonalise(G, steps)
+        err = ref.rel_norm(O, exact)
+        grown = ref.ORTHO[0] ** steps / r ** 0.5
+        assert err <= 2.0 ** -8 + 2.0 ** -7 + (2.0 ** -21 + min(M, N) * 2.0 ** -29) * grown
+        if r == 1 and min(M, N) < 1024:
+            a, b, c = ref.ORTHO
+            X = G.t() if M > N else G
+            X = X / (X.norm() + 1e-7)
+            for _ in range(steps):
+                A = X @ X.t()
+                X = a * X + (b * A + c * (A @ A)) @ X
+            assert err <= 2.0 ** -8 + 2.0 ** -7 + ref.rel_norm(X.t() if M > N else X, exact)
+
+
+@pytest.mark.parametrize("M,N", [(1, 16384), (100, 16000), (200, 16384), (16384, 150)])
+def test_one_entry_alone_is_the_largest_value_that_is_stored(M, N):
+    # X's largest entry is its largest singular value where G has a single one; exact: the scalar iteration
+    G = torch.zeros(1, M, N, device="cuda")
+    G[0, M // 2, N // 3] = -3.0
+    for steps, (a, b, c) in ((5, ref.ORTHO), (2, (4.5, 0.0, 0.0)), (3, (1.9, 0.0, 0.0))):
+        if b == 0.0:
+            c, a = 0.0, min(a, 8.0 ** (1 / steps))         # singular values up to 8 at the end
+        x = 1.0
+        for _ in range(steps):
+            x = a * x + b * x ** 3 + c * x ** 5
+        O = done(run(G, 1, M, N, steps=steps, coef=(a, b, c)))
+        assert abs(float(O[0, M // 2, N // 3]) + x) <= (2.0 ** -8 + 2.0 ** -7) * x
+        assert int((O != 0).sum()) == 1

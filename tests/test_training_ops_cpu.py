@@ -278,3 +278,19 @@ def test_binding_refuses_other_types_and_smaller_tensors(L, op):
     if "token_mask" in good:
         with pytest.raises(ValueError, match="CUDA tensors"):
             call(dict(good, token_mask=good["token_mask"].bool()))
+
+
+@pytest.mark.parametrize("M,N,merged", [(128, 700, False), (300, 200, False), (512, 1024, True)])
+@pytest.mark.parametrize("r", [1, 8])
+@pytest.mark.parametrize("steps", [8, 10, 12])
+def test_noise_outside_a_low_rank_stays_at_what_22_bits_of_x_leave(M, N, merged, r, steps):
+    # Each value of X is off by at most 2^-22 of it; in the directions G lacks a^steps multiplies that. As much comes from the
+    # products: B, rounded by at most 2^-11 of it, times what the first fp16 value lacks of X, at most 2^-11 of that, and |B|
+    # is below a (the first two steps at once: Q in its place, below a^2, of growth a^2). 2^-21 in all. The bounds are reached
+    # only where roundings line up (few distinct values, as here), the average is a quarter, which leaves room for the noise
+    # of later steps and for singular values that end at 0.7.
+    G = ref.low_rank(M, N, r)
+    exact = ref.orthogonalise(G, steps)
+    err = lambda spare: ref.rel_norm(ref.orthogonalise_model(G, steps, merged=merged, spare=spare), exact)
+    assert err(5) <= 2.0 ** -21 * ref.ORTHO[0] ** steps / r ** 0.5 + 2.0 ** -8
+    assert steps < 10 or err(5) < err(0)

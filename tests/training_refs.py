@@ -72,16 +72,16 @@ def orthogonalise(G, steps=5, coef=ORTHO, eps=1e-7):
     return X.t() if tall else X
 
 
-def orthogonalise_model(G, steps=5, coef=ORTHO, eps=1e-7, merged=False):
+def orthogonalise_model(G, steps=5, coef=ORTHO, eps=1e-7, merged=False, spare=0):
     """The same with the kernel's roundings, sums in 64 bits: products of fp16 X, 64 A and 64 B; X carried as two
-    fp16 values that both enter a X; X times a power of two near the square root of the longer side. merged: the
-    first two steps at once, as large matrices take them."""
+    fp16 values that both enter a X; X times a power of two near the square root of the longer side, and `spare` bits more
+    (the kernel's: 5). merged: the first two steps at once, as large matrices take them."""
     a, b, c = coef
     h = lambda t: t.to(torch.float16).double()
     X = G.double()
     tall = X.shape[0] > X.shape[1]
     X = X.t() if tall else X
-    S = 2.0 ** np.floor(0.5 * np.log2(max(X.shape)) + 0.5)
+    S = 2.0 ** (np.floor(0.5 * np.log2(max(X.shape)) + 0.5) + spare)
     X = X / (X.norm() + eps) * S
     if merged:
         hi = h(X)
@@ -98,6 +98,13 @@ def orthogonalise_model(G, steps=5, coef=ORTHO, eps=1e-7, merged=False):
         X = a * (hi + h(X - hi)) + Q @ hi / 64
     X = X / S
     return X.t() if tall else X
+
+
+def low_rank(M, N, r, seed=0, device="cpu"):
+    """A matrix of exactly rank r in fp32: products of small whole numbers."""
+    g = torch.Generator().manual_seed(seed + 1000 * M + N + r)
+    u, v = (torch.randint(-9, 10, s, generator=g).float() for s in ((M, r), (r, N)))
+    return (u @ v).to(device)
 
 
 def rel_norm(x, y):
