@@ -5,8 +5,9 @@
 // about the same, so both products run on the tensor cores and dx is bound by its own traffic.
 //
 //  1. Preparation. dl goes into three bf16 parts (8 + 8 + 8 bits, all of fp32) for dWg, with partial column sums for
-//     db. W_g goes into two, and dx = d1 w1 + d1 w2 + d2 w1: off by 2^-18 of a term or three. Fewer bits would show:
-//     rows of a softmax's gradient sum to zero, so what W_g's rows share cancels while its rounding errors do not (a
+//     db. W_g goes into two, and dx = d1 w1 + d1 w2 + d2 w1: a term is off by 2^-18 of it on average, 3 2^-16 at most
+//     (half a step of bf16, 2^-8, twice over; three times: W_g's rest, dl's, d2 w2). Fewer bits would show: rows of a
+//     softmax's gradient sum to zero, so what W_g's rows share cancels while its rounding errors do not (256 experts, a
 //     shared row of 100 times their spread: fp16 operands leave dx 2.6e-2 off, these 4e-4, its own rounding is 1.7e-3).
 //     bf16 needs no scales: nothing has to be known before the parts are made, so this is one launch.
 //  2. router_products_kernel, dx: a CTA keeps its W_g panel (all experts x 256 or 128 columns) in shared memory and

@@ -409,7 +409,8 @@ moe_status_t moe_balance_loss_backward(int T, int E, int k, const float* logits,
  * The products run on the tensor cores: dWg with dlogits in three bf16 parts
  * (its 24 bits) against x, sums promoted to fp32 registers every 128 tokens;
  * dx with W_g and dlogits in two bf16 parts each (16 bits: a term is off by at
- * most 3 2^-18 of it, whatever its size within fp32's normal range), fp32 sums.
+ * most 3 2^-16 of it, by 2^-18 on average, whatever its size within fp32's normal
+ * range), fp32 sums.
  * Up to 512 tokens and 2^25 products T H E both run in fp32 on the CUDA cores.
  * Results repeat bit for bit.
  * A dlogits row of zeros leaves its dx row at dx0. Values beyond 3e38 count as
