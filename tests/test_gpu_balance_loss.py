@@ -319,3 +319,21 @@ def test_runs_of_tokens_are_joined_in_64_bits():
         want = np.full(E, m / 512.0) / n
         want[0] = (n - m + m / 512.0) / n
         assert np.array_equal(to_np(mp)[0], want.astype(np.float32)), seed
+
+
+@pytest.mark.parametrize("T,E,S", [(2600, 16, 2600), (9000, 8, 3001), (4000, 60, 5000), (300, 12, 3000), (2500, 4, 65535)])
+def test_thousands_of_sequences(T, E, S):
+    # beyond 1024 (backward) and 2048 (forward) sequences a block's first one is searched for; up to the limit of S
+    r = np.random.default_rng(S)
+    off = np.arange(T + 1) if S == T else np.concatenate([[2], np.sort(r.integers(2, T - 5, S - 1)), [T - 5]])
+    mask = None if S == T else (r.random(T) > 0.2).astype(np.uint8)
+    Case(T, E, min(2, E), off=off, mask=mask).forward().backward().check()
+
+
+def test_bad_offsets_of_thousands_of_sequences_stay_in_bounds():
+    T, S = 3000, 2500
+    c = Case(T, 16, 2, off=list(range(S + 1)))
+    c.d_off.copy_(torch.randint(-2 ** 31, 2 ** 31 - 1, (S + 1,), generator=torch.Generator().manual_seed(1), dtype=torch.int64).int())
+    c.forward().backward()
+    torch.cuda.synchronize()
+    assert api.moe_get_device_status() == api.MOE_ERR_CAPACITY
