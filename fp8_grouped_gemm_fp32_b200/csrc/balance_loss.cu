@@ -18,8 +18,10 @@
 // memory's pace. The forward cuts the tokens into at most 296 chunks (two blocks an SM); chunk c of sequence s
 // leaves one row of partial sums at index c + s, which is unique because the cuts between chunks and sequences,
 // taken in order, each move c or s up by one. No float is added atomically, so results repeat bit for bit.
-// Measured on a B200, replayed: 128 x 256 forward and backward 9.8 us, 8192 x 256 13.3 us (launches); 65536 x 512
-// forward 33 us (134 MB: 4.1 TB/s, about 10 us of it the two launches' fixed cost), backward 47 us (268 MB: 5.7 TB/s).
+// Measured on a B200, replayed: 128 x 256 forward and backward 9.9 us, 8192 x 256 14.6 us (launches); 65536 x 512
+// 84 us, of it 33 the forward's read (134 MB: 4.1 TB/s), 12 its join, 42 the gradient (134 MB read and as many written).
+// The gradient reads the logits again because it is a call of its own: its factors come from topk_idx, the mask, the
+// offsets and dloss, not from the loss. The one-launch form spills 56 bytes a thread where E is no multiple of 4.
 #include <math.h>
 
 #include <algorithm>

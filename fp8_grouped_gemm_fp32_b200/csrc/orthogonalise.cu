@@ -28,7 +28,7 @@
 // less for these two). A later pair must not: A_2 then carries A_1's rounding noise, grown by a^2, into directions
 // that the products with X would have resolved (2 to 3 times the error); in the first pair it does not show.
 //
-// Measured on a B200, 5 steps: four of 4096 x 2048 984 us (1.22 PFLOP/s, symmetric products counted half), 1186 us when
+// Measured on a B200, 5 steps: four of 4096 x 2048 1009 us (1.19 PFLOP/s, symmetric products counted half), 1220 us when
 // run on and on under the power cap (1.2 - 1.4 GHz): a K block takes 633 to 709 cycles, its MMAs 512. Sixteen of 256 x 512
 // 97 us: 15 products one after another at 6.6 us (12,700 cycles), of which the MMAs of K = 512 at 32 KB a K block take
 // 4600, the epilogue 750 (A) to 2200 (update), its stores and their release 2500, the next tile's poll and first loads
@@ -720,9 +720,11 @@ ortho_convert_kernel(const void* __restrict__ G, int M, int N, int ldx, int inte
 // crosses between CTAs, once a step. Each CTA owns 128 columns of Y (X, or X^T where G is tall: s rows, l columns), in
 // fp32 registers, with their fp16 values as an MMA operand in shared memory; it computes A over all of Y itself (all
 // CTAs of a matrix the same bits: one order of K blocks), then B, in shared memory too, and its columns of the update.
-// The first exchange is the partial sums of |G|^2. Measured on a B200 (us, against the kernel above with its two
-// preparing launches): 64 x 64 28 / 64, 148 of them 29 / 130, 8 of 128 x 256 49 / 78, 2 of 100 x 1000 70 / 101,
-// 128 x 4096 153 / 167, 64 of 128 x 512 116 / 134. A step is 5500 cycles and an exchange 5000 to 7000 more.
+// The first exchange is the partial sums of |G|^2. Measured on a B200 (us in turn, graphs of ten calls, against the kernel
+// above with its two preparing launches): 64 x 64 28 / 56, 148 of them 31 / 129, 8 of 128 x 256 52 / 79, 2 of 100 x 1000
+// 70 / 101, 128 x 4096 158 / 165, 64 of 128 x 512 119 / 135. A step is 5500 cycles and an exchange 5000 to 7000 more. A
+// thread's 64 values of X, 32 words of an operand and the norm's fp64 sums exceed its 168 registers: 310 (fp32) to 406
+// (bf16) bytes of spills.
 constexpr int kNStages = 5;
 
 struct SmemN {
@@ -1047,9 +1049,10 @@ int wave_of(int mats, int M, int N, int interleaved) {
     return w;
 }
 
-// The first two steps at once. Measured on a B200 (us, step by step / merged): two of 2048 x 7168 910 / 815, four of
-// 4096 x 2048 1069 / 984, one of 2048 x 4096 400 / 396, four of 1024 x 2048 251 / 257: below 1024 the one product more
-// in a row costs what the flops save.
+// The first two steps at once. Measured on a B200 (us in turn, step by step / merged; graphs of ten calls, and for a second
+// on and on under the power cap): two of 2048 x 7168 932 / 824 and 1118 / 991, four of 4096 x 2048 1090 / 1009 and
+// 1322 / 1220, one of 2048 x 4096 411 / 403 and 419 / 407, four of 1024 x 2048 253 / 259 and 259 / 259: below 1024 the one
+// product more in a row costs what the flops save.
 bool merges(int M, int N) { return std::min(M, N) >= 1024 && 2 * std::max(M, N) >= 3 * std::min(M, N); }
 
 struct OrthoWs {

@@ -21,9 +21,11 @@
 //     (unique: both only rise), and
 //  3. router_finish_kernel adds the partial tiles in order, and db. No float atomics: results repeat.
 //
-// Measured on a B200: 8192 x 7168 x 256 188 us a call among others (383 MB; 180 GFLOP of MMAs, where the power cap takes
-// the clock to 1.2 - 1.6 GHz; 150 us with one fp16 product for dx, which lost the bits named above), 4096 x 4096 x 64 34 us (products 28: dx's traffic, and filling two
-// pipelines), 5003 x 1408 x 100 30 us (latency of three launches), 256 x 512 x 8 4.8 us (one launch).
+// Measured on a B200, replayed: 8192 x 7168 x 256 159 us (383 MB; 180 GFLOP of MMAs, 148 us of it the products at 1.2
+// PFLOP/s, where the power cap takes the clock to 1.6 GHz in one launch and below in many: 189 us a call among others;
+// with one fp16 product for dx, which lost the bits named above, 125 and 150), 4096 x 4096 x 64 34.6 us (products 28: dx's
+// traffic, and filling two pipelines), 5003 x 1408 x 100 28.5 us (latency of three launches), 256 x 512 x 8 4.9 us (one
+// launch). The products' 232 registers a thread leave 20 to 28 bytes of spills.
 #include <algorithm>
 
 #include "../../include/moe_fp8.h"

@@ -1,9 +1,8 @@
 """moe_router_backward on the GPU against 64-bit products of the same inputs.
 
-Tolerances. dx: W_g and dlogits each rounded to fp16, at most 2^-11 relative (values far below their row's largest:
-2^-34 of it), exact products, fp32 sums of E terms on the tensor cores (each addition at most 2^-23): so
-(2^-10 + E 2^-23) sum |dl||W| + 2^-33 E max|dl W|, then one rounding to bf16, 2^-8 of the result. (Up to 128 experts
-bf16 pairs, and for few tokens fp32, lie well inside that.) dWg: dlogits in three
+Tolerances. dx: room for operands of 11 bits, (2^-10 + E 2^-23) sum |dl||W| + 2^-33 E max|dl W|, then one rounding to
+bf16, 2^-8 of the result. (W_g and dlogits in bf16 pairs, and for few tokens fp32, lie well inside that; what the pairs
+keep is tested in test_gpu_router_precision.) dWg: dlogits in three
 bf16 parts loses at most 2^-25; sums of 16 products at a time, 128 tokens x 3 parts = 24 additions of at most 2^-23
 before promotion, then one fp32 addition per 128 tokens and per partial tile: (64 + T / 128 + 160) 2^-24 sum |dl||x|.
 db: at most 4 additions a lane, 8 warps, then 64 bits: 16 2^-24 sum |dl|. Bases add one rounding."""
