@@ -337,3 +337,11 @@ def test_bad_offsets_of_thousands_of_sequences_stay_in_bounds():
     c.forward().backward()
     torch.cuda.synchronize()
     assert api.moe_get_device_status() == api.MOE_ERR_CAPACITY
+
+
+@pytest.mark.parametrize("T,E,S", [(200, 8, 65535), (256, 65, 2500)])
+def test_few_tokens_of_thousands_of_sequences(T, E, S):
+    # the one-launch form; most sequences are empty
+    r = np.random.default_rng(S)
+    off = np.concatenate([[0], np.sort(r.integers(0, T, S - 1)), [T - 1]])
+    Case(T, E, 2, off=off).forward().backward().check()
